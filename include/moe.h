@@ -34,14 +34,18 @@
  *       w_down [E, d, I]; shared: ws_gate [I_s, d], ws_up [I_s, d],
  *       ws_down [d, I_s].  I_s == 0 means no shared expert (ws_* ignored).
  *   - Types: activations (x, x_perm, y_perm, y) are MOE_F32 or MOE_BF16;
- *     weights are MOE_F32 (with F32 activations), MOE_BF16, or
+ *     weights are MOE_F32 (with F32 activations), MOE_BF16,
  *     MOE_FP8_E4M3_B128 (bf16 activations; E4M3 codes with one fp32 scale per
- *     128 x 128 block: value = decode(q) * scale[row/128][col/128]).
+ *     128 x 128 block: value = decode(q) * scale[row/128][col/128]), or
+ *     MOE_MXFP4_B32 (bf16 activations; microscaled 4-bit codes, two per byte,
+ *     as moe_mx4_quantize writes them: each matrix [N, K] is N * K / 2 bytes).
  *   - FP8 `scales` packs, in this order: gate [E][I/128][d/128], up (same),
  *     down [E][d/128][I/128], shared gate [I_s/128][d/128], shared up (same),
- *     shared down [d/128][I_s/128].  NULL for non-FP8 weights.
+ *     shared down [d/128][I_s/128].  MXFP4 `scales` packs the same blocks in
+ *     the same order, a 512-byte scale tile each (moe_mx4_quantize's layout).
+ *     NULL for other weights.
  *   - Limits: 1 <= k <= min(E, 16); E <= 512; d, I, I_s multiples of 8
- *     (multiples of 128 for FP8 weights); T >= 0 with T * (k + 1) < 2^31;
+ *     (multiples of 128 for FP8 and MXFP4 weights); T >= 0 with T * (k + 1) < 2^31;
  *     every pointer 16-byte aligned.
  */
 #ifndef MOE_H
@@ -71,7 +75,7 @@ typedef enum {
   MOE_ERR_TIMEOUT = 7               /* device status: a pipeline wait gave up */
 } moe_status;
 
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3_B128 = 2 } moe_dtype;
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3_B128 = 2, MOE_MXFP4_B32 = 3 } moe_dtype;
 
 /* Shapes of one block invocation.  R = T*k routed rows; R' = R + T (I_s > 0)
  * or R (I_s == 0) dispatched rows. */
@@ -125,7 +129,7 @@ MOE_API moe_status moe_permute(const moe_problem* p, const void* x, const int32_
 MOE_API moe_status moe_expert_ffn(const moe_problem* p, const void* x_perm, const int32_t* offs,
                           const void* w_gate, const void* w_up, const void* w_down,
                           const void* ws_gate, const void* ws_up, const void* ws_down,
-                          const float* scales, void* y_perm, void* ws, size_t ws_bytes,
+                          const void* scales, void* y_perm, void* ws, size_t ws_bytes,
                           void* stream);
 
 /* Combine stage (steps 3 and 5: the token's output is the kept experts'
@@ -155,7 +159,7 @@ MOE_API moe_status moe_combine(const moe_problem* p, const void* y_perm, const i
 MOE_API moe_status moe_layer_forward(const moe_problem* p, const void* x, const void* w_router,
                              const float* router_bias, const void* w_gate, const void* w_up,
                              const void* w_down, const void* ws_gate, const void* ws_up,
-                             const void* ws_down, const float* scales, void* y,
+                             const void* ws_down, const void* scales, void* y,
                              int32_t* topk_ids_out, float* topk_w_out, void* ws, size_t ws_bytes,
                              void* stream);
 
@@ -184,7 +188,7 @@ typedef struct {
 MOE_API moe_status moe_block_forward(const moe_problem* p, const moe_block_options* opt, const void* x,
                              const void* w_router, const float* router_bias, const void* w_gate,
                              const void* w_up, const void* w_down, const void* ws_gate,
-                             const void* ws_up, const void* ws_down, const float* scales, void* y,
+                             const void* ws_up, const void* ws_down, const void* scales, void* y,
                              int32_t* topk_ids_out, float* topk_w_out, void* ws, size_t ws_bytes,
                              void* stream);
 
@@ -194,6 +198,54 @@ MOE_API moe_status moe_block_forward(const moe_problem* p, const moe_block_optio
  * x_out 16-byte aligned; eps >= 0 and finite. */
 MOE_API moe_status moe_rmsnorm(const moe_problem* p, const void* x, const void* norm_weight, float eps,
                        void* x_out, void* stream);
+
+/* The whole block for a few tokens (decode steps, speculated tokens): the
+ * computation of moe_block_forward (same arguments; opt may be NULL) for
+ * T <= 16 in one cooperative kernel, preceded by the prologue kernel when
+ * opt asks for the norm or the shared gate.  Where moe_block_forward spends
+ * five or six launches, this one's time is the active experts' weight bytes
+ * plus about ten microseconds.  bf16 activations; BF16, FP8_E4M3_B128 or
+ * MXFP4_B32 weights.  Sums are fp32 throughout: the SwiGLU activation, already
+ * multiplied by the routing weight, is rounded to bf16 once, y once, and the
+ * down projection is one sum over the token's experts, so results differ from
+ * moe_block_forward's in rounding only; they are reproducible bit for bit.  An
+ * infinity or a NaN in the weights of an expert reaches only the tokens routed
+ * to it.  The kernel needs every SM of the device: it starts when earlier work
+ * leaves them free.  ws: moe_decode_workspace_size() bytes, not shared with a
+ * call that may run at the same time.  T > 16 or F32 activations:
+ * MOE_ERR_UNSUPPORTED (use moe_block_forward). */
+MOE_API size_t moe_decode_workspace_size(const moe_problem* p);
+MOE_API moe_status moe_decode_forward(const moe_problem* p, const moe_block_options* opt, const void* x,
+                             const void* w_router, const float* router_bias, const void* w_gate,
+                             const void* w_up, const void* w_down, const void* ws_gate, const void* ws_up,
+                             const void* ws_down, const void* scales, void* y, int32_t* topk_ids_out,
+                             float* topk_w_out, void* ws, size_t ws_bytes, void* stream);
+
+/* Microscaled 4-bit matrices (the MXFP4_B32 weight format; "quantification" to
+ * 4 bits is named on the Fondations page, chapter 06).  x [batch, rows, cols]
+ * (dtype MOE_F32 or MOE_BF16), cols a multiple of 32.
+ *   codes   [batch, rows, cols / 2] bytes: two codes per byte, the
+ *           lower-indexed value in the low half; a code is sign, two exponent
+ *           bits, one mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and negatives;
+ *   scales  moe_mx4_scale_bytes() bytes: one byte b per 32 consecutive values
+ *           of a row, value = code * 2^(b - 127), b = 255 a block of NaN.  Kept
+ *           per tile of 128 rows x 128 columns (tiles along the columns, then
+ *           down the rows, then over the matrices), 512 bytes each: byte
+ *           (r % 32) * 16 + (r / 32) * 4 + c / 32 for row r, column c of the
+ *           tile; 127 past the matrix's end.
+ * Quantisation (OCP MX): b - 127 = floor(log2(max |x|)) - 2, at least -127, of
+ * the block's 32 values; codes rounded to nearest, ties to the even code,
+ * saturating at 6.  A block of zeros takes b = 127, a block holding an infinity
+ * or a NaN b = 255 and codes 0.  moe_mx4_dequantize writes codes * scale in
+ * `dtype` (exact, but for magnitudes past the largest finite value).
+ * Errors: MOE_ERR_INVALID_ARG (sizes, type, NULL), MOE_ERR_ALIGNMENT (a pointer
+ * not 16-byte aligned), MOE_ERR_UNSUPPORTED (a size or the tile count above
+ * 2^31 - 1), all before any launch; batch or rows 0 does nothing. */
+MOE_API size_t moe_mx4_scale_bytes(int64_t batch, int64_t rows, int64_t cols);
+MOE_API moe_status moe_mx4_quantize(const void* x, int32_t dtype, int64_t batch, int64_t rows, int64_t cols,
+                             void* codes, void* scales, void* stream);
+MOE_API moe_status moe_mx4_dequantize(const void* codes, const void* scales, int64_t batch, int64_t rows,
+                             int64_t cols, int32_t dtype, void* out, void* stream);
 
 /* Expert parallelism, receive side.  The block split over G ranks, rank g
  * holding experts [g * E_local, (g + 1) * E_local) (the path's experts are

@@ -14,7 +14,9 @@ given) to be on one device, and runs with that device current.
 
 Entry points mirror ``include/moe.h``: ``router_topk``, ``permute``,
 ``expert_ffn``, ``combine``, ``layer_forward``, ``block_forward``,
-``rmsnorm``, ``ep_expand_ids``; ``MoELayer`` keeps a layer's weights and
+``decode_forward``, ``rmsnorm``, ``ep_expand_ids``, ``quantize_mx4``,
+``dequantize_mx4``; ``quantize_experts_mx4`` turns a block's expert weights
+into the 4-bit ones of w="mx4"; ``MoELayer`` keeps a layer's weights and
 workspace together; ``sparse_moe_layer_top_b200.ep`` splits the experts over
 several GPUs (expert parallelism).
 """
@@ -25,11 +27,12 @@ import os
 import torch
 
 __all__ = ["MoEError", "Problem", "BlockOptions", "router_topk", "permute", "expert_ffn", "combine", "layer_forward",
-           "block_forward", "rmsnorm", "ep_expand_ids", "forward_plan",
+           "block_forward", "decode_forward", "decode_workspace_size", "rmsnorm", "ep_expand_ids", "forward_plan",
+           "quantize_mx4", "dequantize_mx4", "quantize_experts_mx4", "mx4_scale_tiles",
            "workspace_size", "stage_workspace_size", "set_path", "set_wait_limit", "device_status",
            "last_launch_count", "bounds_checked",
            "profile_enable", "profile_read",
-           "MoELayer", "lib_path", "F32", "BF16", "FP8_E4M3_B128"]
+           "MoELayer", "lib_path", "F32", "BF16", "FP8_E4M3_B128", "MXFP4_B32", "DECODE_MAX_T"]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 # MOE_CHECKS=1 loads the bounds-checking build (python -m
@@ -37,14 +40,17 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 # computed indices on the device (moe_bounds_checked in include/moe.h)
 lib_path = os.path.join(HERE, "libmoe_checks.so" if os.environ.get("MOE_CHECKS") == "1" else "libmoe.so")
 
-F32, BF16, FP8_E4M3_B128 = 0, 1, 2
+F32, BF16, FP8_E4M3_B128, MXFP4_B32 = 0, 1, 2, 3
+DECODE_MAX_T = 16  # most tokens decode_forward takes
 _STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_ALIGNMENT",
            4: "MOE_ERR_WORKSPACE_TOO_SMALL", 5: "MOE_ERR_CUDA", 6: "MOE_ERR_DEVICE_CHECK", 7: "MOE_ERR_TIMEOUT"}
 EXPORTS = ("moe_check_problem", "moe_workspace_size", "moe_stage_workspace_size", "moe_router_topk",
            "moe_permute", "moe_expert_ffn", "moe_combine", "moe_layer_forward", "moe_set_path",
            "moe_device_status", "moe_last_launch_count", "moe_profile_enable", "moe_profile_read",
            "moe_last_error_string", "moe_router_topk_static", "moe_block_forward", "moe_rmsnorm",
-           "moe_ep_expand_ids", "moe_forward_plan", "moe_set_wait_limit", "moe_bounds_checked")
+           "moe_ep_expand_ids", "moe_forward_plan", "moe_set_wait_limit", "moe_bounds_checked",
+           "moe_decode_workspace_size", "moe_decode_forward", "moe_mx4_scale_bytes", "moe_mx4_quantize",
+           "moe_mx4_dequantize")
 
 
 class MoEError(RuntimeError):
@@ -60,7 +66,7 @@ class Problem(ctypes.Structure):
 
     @classmethod
     def make(cls, T, d, E, k, I, I_s, act="bf16", w="bf16"):
-        codes = {"f32": F32, "bf16": BF16, "fp8": FP8_E4M3_B128}
+        codes = {"f32": F32, "bf16": BF16, "fp8": FP8_E4M3_B128, "mx4": MXFP4_B32}
         return cls(int(T), int(d), int(E), int(k), int(I), int(I_s), codes[act], codes[w])
 
 
@@ -92,6 +98,14 @@ def lib():
         L.moe_layer_forward.argtypes = [PP, P, P, P, P, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
         L.moe_block_forward.argtypes = [PP, ctypes.POINTER(BlockOptions), P, P, P, P, P, P, P, P, P, P, P, P, P,
                                         P, ctypes.c_size_t, P]
+        L.moe_decode_workspace_size.argtypes = [PP]
+        L.moe_decode_workspace_size.restype = ctypes.c_size_t
+        L.moe_decode_forward.argtypes = L.moe_block_forward.argtypes
+        I64 = ctypes.c_int64
+        L.moe_mx4_scale_bytes.argtypes = [I64, I64, I64]
+        L.moe_mx4_scale_bytes.restype = ctypes.c_size_t
+        L.moe_mx4_quantize.argtypes = [P, ctypes.c_int32, I64, I64, I64, P, P, P]
+        L.moe_mx4_dequantize.argtypes = [P, P, I64, I64, I64, ctypes.c_int32, P, P]
         L.moe_ep_expand_ids.argtypes = [P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int64, P, P]
         I32P = ctypes.POINTER(ctypes.c_int32)
         L.moe_forward_plan.argtypes = [PP, I32P, I32P, I32P]
@@ -109,7 +123,7 @@ def lib():
         L.moe_last_error_string.restype = ctypes.c_char_p
         for f in ("moe_check_problem", "moe_router_topk", "moe_router_topk_static", "moe_permute", "moe_expert_ffn", "moe_combine",
                   "moe_layer_forward", "moe_block_forward", "moe_rmsnorm", "moe_set_path", "moe_device_status",
-                  "moe_set_wait_limit"):
+                  "moe_set_wait_limit", "moe_decode_forward", "moe_mx4_quantize", "moe_mx4_dequantize"):
             getattr(L, f).restype = S
         _lib = L
     return _lib
@@ -122,7 +136,8 @@ def _check(status):
 
 _F32, _I32 = (torch.float32,), (torch.int32,)
 _ACT_TYPES = {F32: (torch.float32,), BF16: (torch.bfloat16,)}
-_W_TYPES = {F32: (torch.float32,), BF16: (torch.bfloat16,), FP8_E4M3_B128: (torch.float8_e4m3fn, torch.uint8)}
+_W_TYPES = {F32: (torch.float32,), BF16: (torch.bfloat16,), FP8_E4M3_B128: (torch.float8_e4m3fn, torch.uint8),
+            MXFP4_B32: (torch.uint8,)}
 
 
 def _need(t, name, n, dtypes, row=None):
@@ -142,16 +157,19 @@ def _need(t, name, n, dtypes, row=None):
 def _need_weights(prob, wg, wu, wd, s_wg, s_wu, s_wd, scales):
     d, E, I, I_s = prob.d, prob.E, prob.I, prob.I_s
     wt = _W_TYPES.get(prob.w_dtype)
-    _need(wg, "w_gate", E * I * d, wt, d)
-    _need(wu, "w_up", E * I * d, wt, d)
-    _need(wd, "w_down", E * d * I, wt, I)
+    per = 2 if prob.w_dtype == MXFP4_B32 else 1  # values per tensor element
+    _need(wg, "w_gate", E * I * d // per, wt, d // per)
+    _need(wu, "w_up", E * I * d // per, wt, d // per)
+    _need(wd, "w_down", E * d * I // per, wt, I // per)
     if I_s > 0:
-        _need(s_wg, "ws_gate", I_s * d, wt, d)
-        _need(s_wu, "ws_up", I_s * d, wt, d)
-        _need(s_wd, "ws_down", d * I_s, wt, I_s)
+        _need(s_wg, "ws_gate", I_s * d // per, wt, d // per)
+        _need(s_wu, "ws_up", I_s * d // per, wt, d // per)
+        _need(s_wd, "ws_down", d * I_s // per, wt, I_s // per)
+    blocks = 3 * E * (I // 128) * (d // 128) + (3 * (I_s // 128) * (d // 128) if I_s > 0 else 0)
     if prob.w_dtype == FP8_E4M3_B128:
-        blocks = 3 * E * (I // 128) * (d // 128) + (3 * (I_s // 128) * (d // 128) if I_s > 0 else 0)
         _need(scales, "scales", blocks, _F32)
+    elif prob.w_dtype == MXFP4_B32:
+        _need(scales, "scales", blocks * MX4_TILE_BYTES, (torch.uint8,))
 
 
 def _nbytes(t):
@@ -260,6 +278,12 @@ def profile_read(max_launches=4096):
     names = (ctypes.c_char_p * max_launches)()
     n = lib().moe_profile_read(max_launches, ms, names)
     return [(names[i].decode(), float(ms[i])) for i in range(n)]
+
+
+def _alloc(stream):
+    """A context in which new tensors belong to `stream`, the stream that uses
+    them first (nothing to do for None, the current one)."""
+    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
 
 
 def _ws(nbytes, device, ws):
@@ -458,8 +482,139 @@ def ep_expand_ids(counts, G, E_local, R, ids=None, stream=None):
     return ids
 
 
+MX4_TILE_BYTES = 512  # scale bytes of 128 x 128 values
+_MX4_FLOAT = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _mx4_shape(shape):
+    """(batch, rows, cols) of a stack of matrices."""
+    if len(shape) < 2:
+        raise ValueError("x: a matrix or a stack of matrices, got %d dimension(s)" % len(shape))
+    batch = 1
+    for n in shape[:-2]:
+        batch *= n
+    return batch, shape[-2], shape[-1]
+
+
+def _mx4_scale_shape(shape):
+    return tuple(shape[:-2]) + ((shape[-2] + 127) // 128, (shape[-1] + 127) // 128, MX4_TILE_BYTES)
+
+
+def quantize_mx4(x, codes=None, scales=None, stream=None):
+    """Microscaled 4-bit codes of x [..., rows, cols] (bf16 or fp32, cols a
+    multiple of 32) -> (codes uint8 [..., rows, cols / 2], scales uint8
+    [..., ceil(rows / 128), ceil(cols / 128), 512]); the layouts and the
+    rounding are those of moe_mx4_quantize in include/moe.h."""
+    batch, rows, cols = _mx4_shape(x.shape)
+    if x.dtype not in _MX4_FLOAT:
+        raise ValueError("x: element type %s, expected torch.float32 or torch.bfloat16" % x.dtype)
+    if cols <= 0 or cols % 32:
+        raise ValueError("x: rows of %d elements, expected a multiple of 32" % cols)
+    sshape = _mx4_scale_shape(x.shape)
+    n = batch * sshape[-3] * sshape[-2] * MX4_TILE_BYTES
+    _need(codes, "codes", batch * rows * cols // 2, (torch.uint8,), cols // 2)
+    _need(scales, "scales", n, (torch.uint8,), MX4_TILE_BYTES)
+    cur = _device(stream, x=x, codes=codes, scales=scales)
+    with _current(cur), _alloc(stream):
+        if codes is None:
+            codes = torch.empty(tuple(x.shape[:-1]) + (cols // 2,), dtype=torch.uint8, device=x.device)
+        if scales is None:
+            scales = torch.empty(sshape, dtype=torch.uint8, device=x.device)
+        _check(lib().moe_mx4_quantize(_ptr(x), _MX4_FLOAT[x.dtype], batch, rows, cols, _ptr(codes), _ptr(scales),
+                                      _stream(stream)))
+    return codes, scales
+
+
+def dequantize_mx4(codes, scales, out=None, dtype=torch.bfloat16, stream=None):
+    """The values codes * scale of quantize_mx4's outputs, in bf16 or fp32 (exact)."""
+    if codes.dtype != torch.uint8:
+        raise ValueError("codes: element type %s, expected torch.uint8" % codes.dtype)
+    shape = _mx4_shape(codes.shape) and tuple(codes.shape[:-1]) + (2 * codes.shape[-1],)
+    batch, rows, cols = _mx4_shape(shape)
+    if cols <= 0 or cols % 32:
+        raise ValueError("codes: rows of %d bytes, expected a multiple of 16" % codes.shape[-1])
+    if out is not None:
+        dtype = out.dtype
+    if dtype not in _MX4_FLOAT:
+        raise ValueError("out: element type %s, expected torch.float32 or torch.bfloat16" % dtype)
+    sshape = _mx4_scale_shape(shape)
+    _need(scales, "scales", batch * sshape[-3] * sshape[-2] * MX4_TILE_BYTES, (torch.uint8,))
+    _need(out, "out", batch * rows * cols, (dtype,), cols)
+    cur = _device(stream, codes=codes, scales=scales, out=out)
+    with _current(cur), _alloc(stream):
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=codes.device)
+        _check(lib().moe_mx4_dequantize(_ptr(codes), _ptr(scales), batch, rows, cols, _MX4_FLOAT[dtype], _ptr(out),
+                                        _stream(stream)))
+    return out
+
+
+def mx4_scale_tiles(scales):
+    """Row-major scale bytes [..., rows, cols / 32] (how checkpoints usually
+    keep them) in the tile layout of quantize_mx4; rows and cols multiples of 128."""
+    if scales.dtype != torch.uint8 or scales.dim() < 2 or scales.shape[-2] % 128 or scales.shape[-1] % 4:
+        raise ValueError("scales: uint8 [..., rows, cols / 32] with rows and cols multiples of 128")
+    lead, n = scales.shape[:-2], scales.dim() - 2
+    t = scales.reshape(lead + (scales.shape[-2] // 128, 4, 32, scales.shape[-1] // 4, 4))
+    t = t.permute(tuple(range(n)) + (n, n + 3, n + 2, n + 1, n + 4))
+    return t.reshape(lead + (scales.shape[-2] // 128, scales.shape[-1] // 4, MX4_TILE_BYTES)).contiguous()
+
+
+def quantize_experts_mx4(wg, wu, wd, s_wg=None, s_wu=None, s_wd=None, stream=None):
+    """A block's expert weights in 4 bits: the six code tensors (None where the
+    shared expert's are None), then the packed scales, as layer_forward,
+    decode_forward and MoELayer take them with w="mx4"."""
+    codes, scales = [], []
+    for w in (wg, wu, wd, s_wg, s_wu, s_wd):
+        if w is None:
+            codes.append(None)
+            continue
+        if w.shape[-1] % 128 or w.shape[-2] % 128:
+            raise ValueError("expert weights %s: the block needs multiples of 128" % (tuple(w.shape),))
+        q, s = quantize_mx4(w, stream=stream)
+        codes.append(q)
+        scales.append(s.reshape(-1))
+    with _current(wg.device), _alloc(stream):
+        packed = torch.cat(scales)
+    return (*codes, packed)
+
+
+def decode_workspace_size(prob):
+    return lib().moe_decode_workspace_size(ctypes.byref(prob))
+
+
+def decode_forward(prob, x, w_router, bias, wg, wu, wd, s_wg=None, s_wu=None, s_wd=None, scales=None,
+                   norm_weight=None, norm_eps=1e-6, shared_gate=None, y=None, topk_ids=None, topk_w=None, ws=None,
+                   stream=None):
+    """block_forward for at most DECODE_MAX_T tokens in one kernel (two with the
+    norm or the gate): the latency form.  ws: decode_workspace_size bytes."""
+    _need_params(prob, w_router, bias, wg, wu, wd, s_wg, s_wu, s_wd, scales, norm_weight, shared_gate)
+    _need_tokens(prob, x, y, topk_ids, topk_w)
+    return _decode(prob, x, w_router, bias, wg, wu, wd, s_wg, s_wu, s_wd, scales, norm_weight, norm_eps, shared_gate,
+                   y, topk_ids, topk_w, ws, stream)
+
+
+def _decode(prob, x, w_router, bias, wg, wu, wd, s_wg, s_wu, s_wd, scales, norm_weight, norm_eps, shared_gate, y,
+            topk_ids, topk_w, ws, stream):
+    cur = _device(stream, x=x, w_router=w_router, router_bias=bias, w_gate=wg, w_up=wu, w_down=wd, ws_gate=s_wg,
+                  ws_up=s_wu, ws_down=s_wd, scales=scales, norm_weight=norm_weight, shared_gate=shared_gate, y=y,
+                  topk_ids=topk_ids, topk_w=topk_w, ws=ws)
+    with _current(cur), _alloc(stream):
+        if y is None:
+            y = torch.empty((prob.T, prob.d), dtype=_act(prob), device=x.device)
+        ws = _ws(decode_workspace_size(prob), x.device, ws)
+        opt = BlockOptions(_ptr(norm_weight), float(norm_eps), _ptr(shared_gate))
+        _check(lib().moe_decode_forward(ctypes.byref(prob), ctypes.byref(opt), _ptr(x), _ptr(w_router), _ptr(bias),
+                                        _ptr(wg), _ptr(wu), _ptr(wd), _ptr(s_wg), _ptr(s_wu), _ptr(s_wd),
+                                        _ptr(scales), _ptr(y), _ptr(topk_ids), _ptr(topk_w), _ptr(ws), _nbytes(ws),
+                                        _stream(stream)))
+    return y
+
+
 class MoELayer:
-    """One block's weights plus a workspace sized for up to `max_tokens` tokens."""
+    """One block's weights plus a workspace sized for up to `max_tokens` tokens.
+    Calling it runs the fused forward; ``decode`` the one-kernel form for a few
+    tokens, in a workspace of its own."""
 
     def __init__(self, d, E, k, I, I_s, w_router, wg, wu, wd, s_wg=None, s_wu=None, s_wd=None, bias=None,
                  scales=None, act="bf16", w="bf16", max_tokens=0, norm_weight=None, norm_eps=1e-6,
@@ -472,6 +627,7 @@ class MoELayer:
                      shared_gate)
         self.device = wg.device
         self.ws = None
+        self.ws_decode = None
         if max_tokens:
             self._reserve(max_tokens)
 
@@ -493,6 +649,20 @@ class MoELayer:
         block = norm_weight is not None or shared_gate is not None
         return _forward(prob, x, w_router, bias, wg, wu, wd, s_wg, s_wu, s_wd, scales, norm_weight, norm_eps,
                         shared_gate, y, topk_ids, topk_w, self.ws, stream, block)
+
+    def decode(self, x, y=None, topk_ids=None, topk_w=None, stream=None):
+        """The block on x [T, d], T <= DECODE_MAX_T, in one kernel (decode_forward)."""
+        prob = self.problem(x.shape[0])
+        _need_tokens(prob, x, y, topk_ids, topk_w)
+        n = decode_workspace_size(prob)
+        if self.ws_decode is None or self.ws_decode.numel() < n:
+            # for the largest batch at once: a captured graph keeps its workspace
+            most = max(n, decode_workspace_size(self.problem(DECODE_MAX_T)), 1)
+            self.ws_decode = torch.empty(most, dtype=torch.uint8, device=self.device)
+        w_router, bias, wg, wu, wd, s_wg, s_wu, s_wd, scales = self.w
+        norm_weight, norm_eps, shared_gate = self.opts
+        return _decode(prob, x, w_router, bias, wg, wu, wd, s_wg, s_wu, s_wd, scales, norm_weight, norm_eps,
+                       shared_gate, y, topk_ids, topk_w, self.ws_decode, stream)
 
     @classmethod
     def from_inputs(cls, inp, max_tokens=0):

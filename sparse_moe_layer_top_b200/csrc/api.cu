@@ -14,7 +14,9 @@
 
 #include "../../include/moe.h"
 #include "common.cuh"
+#include "decode.cuh"
 #include "ep.cuh"
+#include "mx4.cuh"
 #include "permute.cuh"
 #include "prologue.cuh"
 #include "router.cuh"
@@ -250,6 +252,10 @@ static cudaError_t launch_router_kc(K kernel, int ctas, cudaStream_t st, const C
   return cudaLaunchKernelEx(&cfg, kernel, x, w, args, npad);
 }
 
+// Dynamic shared memory of k_decode with nb blocks of 8 token columns: two
+// buffers of every warp's partial sums.
+static int decode_smem(int nb) { return 2 * kDecodeWarps * (2 * nb * 4 * 32) * 4; }
+
 static moe_status device_info(DeviceInfo** out) {
   int dev = 0;
   CUDA_TRY(cudaGetDevice(&dev));
@@ -321,6 +327,12 @@ static moe_status device_info(DeviceInfo** out) {
     CUDA_TRY(allow_smem(k_gemm_swap8<true, kTcSwiGLU>, Swap8Cfg<true>::SMEM_BYTES));
     CUDA_TRY(allow_smem(k_gemm_swap8<true, kTcSlotStore>, Swap8Cfg<true>::SMEM_BYTES));
     CUDA_TRY(allow_smem(k_gemm_swap8<true, kTcStore>, Swap8Cfg<true>::SMEM_BYTES));
+    CUDA_TRY(allow_smem(k_decode<kDecBf16, 1>, decode_smem(1)));
+    CUDA_TRY(allow_smem(k_decode<kDecBf16, 2>, decode_smem(2)));
+    CUDA_TRY(allow_smem(k_decode<kDecFp8, 1>, decode_smem(1)));
+    CUDA_TRY(allow_smem(k_decode<kDecFp8, 2>, decode_smem(2)));
+    CUDA_TRY(allow_smem(k_decode<kDecMx4, 1>, decode_smem(1)));
+    CUDA_TRY(allow_smem(k_decode<kDecMx4, 2>, decode_smem(2)));
     d.ready = true;
   }
   *out = &d;
@@ -397,16 +409,19 @@ static moe_status check(const moe_problem* p) {
   if (p->k > p->E || p->k > kMaxK) return fail(MOE_ERR_INVALID_ARG, "k = %d must be <= min(E, %d)", p->k, kMaxK);
   if (p->act_dtype != MOE_F32 && p->act_dtype != MOE_BF16)
     return fail(MOE_ERR_INVALID_ARG, "activation type %d is not F32 or BF16", p->act_dtype);
-  if (p->w_dtype != MOE_F32 && p->w_dtype != MOE_BF16 && p->w_dtype != MOE_FP8_E4M3_B128)
+  if (p->w_dtype != MOE_F32 && p->w_dtype != MOE_BF16 && p->w_dtype != MOE_FP8_E4M3_B128 &&
+      p->w_dtype != MOE_MXFP4_B32)
     return fail(MOE_ERR_INVALID_ARG, "weight type %d unknown", p->w_dtype);
   if (p->act_dtype == MOE_F32 && p->w_dtype != MOE_F32)
     return fail(MOE_ERR_UNSUPPORTED, "F32 activations need F32 weights");
   if (p->act_dtype == MOE_BF16 && p->w_dtype == MOE_F32)
-    return fail(MOE_ERR_UNSUPPORTED, "BF16 activations take BF16 or FP8 weights");
+    return fail(MOE_ERR_UNSUPPORTED, "BF16 activations take BF16, FP8 or MXFP4 weights");
   if (p->d % 8 || p->I % 8 || p->I_s % 8)
     return fail(MOE_ERR_ALIGNMENT, "d, I, I_s must be multiples of 8 (16-byte rows)");
   if (p->w_dtype == MOE_FP8_E4M3_B128 && (p->d % 128 || p->I % 128 || p->I_s % 128))
     return fail(MOE_ERR_INVALID_ARG, "FP8 block scales need d, I, I_s multiples of 128");
+  if (p->w_dtype == MOE_MXFP4_B32 && (p->d % 128 || p->I % 128 || p->I_s % 128))
+    return fail(MOE_ERR_INVALID_ARG, "MXFP4 scale tiles need d, I, I_s multiples of 128");
   if (p->T * (int64_t)(p->k + 1) >= (int64_t)1 << 31) return fail(MOE_ERR_UNSUPPORTED, "T*(k+1) >= 2^31");
   return MOE_OK;
 }
@@ -683,19 +698,22 @@ static moe_status launch_dispatch(const moe_problem& p, const int32_t* ids, cons
 
 struct ExpertWeights {
   const void *wg, *wu, *wd, *sg, *su, *sd;
-  const float* scales;
+  const void* scales;
 };
 
-// FP8 scale sub-buffers (see moe.h).
-static void scale_parts(const moe_problem& p, const float* sc, const float* part[6]) {
+// FP8 and MXFP4 scale sub-buffers (see moe.h): one fp32 value, or one 512-byte
+// scale tile, per 128 x 128 block of each matrix.
+static void scale_parts(const moe_problem& p, const void* scales, const void* part[6]) {
   const int64_t gd = p.d / 128, gi = p.I / 128, gs = p.I_s / 128;
+  const int64_t unit = p.w_dtype == MOE_MXFP4_B32 ? kMxTileBytes : (int64_t)sizeof(float);
+  const char* sc = static_cast<const char*>(scales);
   const int64_t off[6] = {0,
                           (int64_t)p.E * gi * gd,
                           2 * (int64_t)p.E * gi * gd,
                           3 * (int64_t)p.E * gi * gd,
                           3 * (int64_t)p.E * gi * gd + gs * gd,
                           3 * (int64_t)p.E * gi * gd + 2 * gs * gd};
-  for (int i = 0; i < 6; ++i) part[i] = sc ? sc + off[i] : nullptr;
+  for (int i = 0; i < 6; ++i) part[i] = sc ? sc + off[i] * unit : nullptr;
 }
 
 // Output of the down projection: either the weighted rows in (token, slot)
@@ -735,7 +753,7 @@ template <typename TA, typename TW>
 static moe_status simt_gemms(const moe_problem& p, const void* xp, const int32_t* offs, const ExpertWeights& w,
                              int32_t* pre_a, int32_t* pre_b, void* H, const DownOut& o, cudaStream_t st,
                              DeviceInfo* dev) {
-  const float* sp[6];
+  const void* sp[6];
   scale_parts(p, w.scales, sp);
   const unsigned grid = (unsigned)dev->sms * 4;
   SimtGemmArgs<TA, TW> a{};
@@ -817,7 +835,7 @@ static moe_status tc_gemms_t(const moe_problem& p, const void* xp, const int32_t
   constexpr int S = FP8 ? kFp8Stages : 4;
   using C1 = TcGemmCfg<128, true, S, FP8>;
   using C2 = TcGemmCfg<256, false, S, FP8>;
-  const float* sp[6];
+  const void* sp[6];
   scale_parts(p, w.scales, sp);
   moe_status s;
   CUtensorMap aR, aS, bR, bS, cR, cS;
@@ -846,10 +864,10 @@ static moe_status tc_gemms_t(const moe_problem& p, const void* xp, const int32_t
   a.out_keep = keep_out(Rp * ldh * 2);
   a.panel = panel_of(2 * 128 * (int64_t)p.d * (FP8 ? 1 : 2), cdiv(p.I, 128));  // gate and up rows, 128 columns
   a.swap_small = FP8 ? 0 : 1;  // tiles of at most 64 rows run with the MMA roles swapped
-  a.sc_b_r = sp[0];
-  a.sc_b_s = sp[3];
-  a.sc_c_r = sp[1];
-  a.sc_c_s = sp[4];
+  a.sc_b_r = (const float*)sp[0];
+  a.sc_b_s = (const float*)sp[3];
+  a.sc_c_r = (const float*)sp[1];
+  a.sc_c_s = (const float*)sp[4];
   a.status = dev->status;
   if (!FP8) a.sched = pre_a + p.E + 2;  // tiles claimed in order (the prefix writer zeroed it)
   PROF_BEGIN("gemm_tc_swiglu", st);
@@ -882,8 +900,8 @@ static moe_status tc_gemms_t(const moe_problem& p, const void* xp, const int32_t
   b.N_s = p.d;
   b.K_r = p.I;
   b.K_s = p.I_s;
-  b.sc_b_r = sp[2];
-  b.sc_b_s = sp[5];
+  b.sc_b_r = (const float*)sp[2];
+  b.sc_b_s = (const float*)sp[5];
   b.status = dev->status;
   b.out_keep = keep_out((o.ys ? p.T * (p.k + 1) : Rp) * p.d * 2);
   b.panel = panel_of(256 * (int64_t)std::max(p.I, p.I_s) * (FP8 ? 1 : 2), cdiv(p.d, 256));
@@ -931,7 +949,7 @@ static moe_status swap_gemms_t(const moe_problem& p, const void* xp, const int32
   using C2 = SwapCfg<false>;
   const int64_t Rp = rows_total(p), ldh = ldh_of(p);
   const bool sh = p.I_s > 0;
-  const float* sp[6];
+  const void* sp[6];
   scale_parts(p, w.scales, sp);
   moe_status s;
   CUtensorMap xR, xS, bR, bS, cR, cS;
@@ -958,10 +976,10 @@ static moe_status swap_gemms_t(const moe_problem& p, const void* xp, const int32
     a.K_s = p.d;
     a.H = (bf16*)H;
     a.ldh = ldh;
-    a.sc_b_r = sp[0];
-    a.sc_b_s = sp[3];
-    a.sc_c_r = sp[1];
-    a.sc_c_s = sp[4];
+    a.sc_b_r = (const float*)sp[0];
+    a.sc_b_s = (const float*)sp[3];
+    a.sc_c_r = (const float*)sp[1];
+    a.sc_c_s = (const float*)sp[4];
     a.status = dev->status;
     PROF_BEGIN("gemm_tc_swiglu", st);
     if (FP8)
@@ -990,10 +1008,10 @@ static moe_status swap_gemms_t(const moe_problem& p, const void* xp, const int32
   b.N_s = p.d;
   b.K_r = p.I;
   b.K_s = p.I_s;
-  b.sc_b_r = sp[2];
-  b.sc_b_s = sp[5];
-  b.sc_c_r = sp[2];  // E4M3: the second 128-row half of each 256-row tile, same matrix
-  b.sc_c_s = sp[5];
+  b.sc_b_r = (const float*)sp[2];
+  b.sc_b_s = (const float*)sp[5];
+  b.sc_c_r = (const float*)sp[2];  // E4M3: the second 128-row half of each 256-row tile, same matrix
+  b.sc_c_s = (const float*)sp[5];
   b.status = dev->status;
   if (o.ys) {
     b.ys = (bf16*)o.ys;
@@ -1228,6 +1246,7 @@ static moe_status expert_gemms(const moe_problem& p, int form, const void* xp, c
   if (form == kFormPairT) return pairt_gemms(p, xp, offs, w, pre_a, pre_b, H, o, st, dev);
   if (p.act_dtype == MOE_F32) return simt_gemms<float, float>(p, xp, offs, w, pre_a, pre_b, H, o, st, dev);
   if (p.w_dtype == MOE_BF16) return simt_gemms<bf16, bf16>(p, xp, offs, w, pre_a, pre_b, H, o, st, dev);
+  if (p.w_dtype == MOE_MXFP4_B32) return simt_gemms<bf16, mx4>(p, xp, offs, w, pre_a, pre_b, H, o, st, dev);
   return simt_gemms<bf16, uint8_t>(p, xp, offs, w, pre_a, pre_b, H, o, st, dev);
 }
 
@@ -1259,7 +1278,7 @@ static moe_status check_weights(const moe_problem& p, const ExpertWeights& w) {
     NEED(w.su);
     NEED(w.sd);
   }
-  if (p.w_dtype == MOE_FP8_E4M3_B128) NEED(w.scales);
+  if (p.w_dtype == MOE_FP8_E4M3_B128 || p.w_dtype == MOE_MXFP4_B32) NEED(w.scales);
   return MOE_OK;
 }
 
@@ -1401,7 +1420,7 @@ moe_status moe_permute(const moe_problem* p, const void* x, const int32_t* topk_
 
 moe_status moe_expert_ffn(const moe_problem* p, const void* x_perm, const int32_t* offs, const void* w_gate,
                           const void* w_up, const void* w_down, const void* ws_gate, const void* ws_up,
-                          const void* ws_down, const float* scales, void* y_perm, void* ws, size_t ws_bytes,
+                          const void* ws_down, const void* scales, void* y_perm, void* ws, size_t ws_bytes,
                           void* stream) {
   NvtxRange nvtx_("moe_expert_ffn");
   moe_status s = check(p);
@@ -1490,7 +1509,7 @@ static moe_status launch_prologue(const moe_problem& p, const void* x, const voi
 static moe_status block_forward(const moe_problem* p, const moe_block_options* opt, const void* x,
                                 const void* w_router, const float* router_bias, const void* w_gate,
                                 const void* w_up, const void* w_down, const void* ws_gate, const void* ws_up,
-                                const void* ws_down, const float* scales, void* y, int32_t* topk_ids_out,
+                                const void* ws_down, const void* scales, void* y, int32_t* topk_ids_out,
                                 float* topk_w_out, void* ws, size_t ws_bytes, void* stream) {
   NvtxRange nvtx_("moe_layer_forward");
   moe_status s = check(p);
@@ -1587,7 +1606,7 @@ static moe_status block_forward(const moe_problem* p, const moe_block_options* o
 
 moe_status moe_layer_forward(const moe_problem* p, const void* x, const void* w_router, const float* router_bias,
                              const void* w_gate, const void* w_up, const void* w_down, const void* ws_gate,
-                             const void* ws_up, const void* ws_down, const float* scales, void* y,
+                             const void* ws_up, const void* ws_down, const void* scales, void* y,
                              int32_t* topk_ids_out, float* topk_w_out, void* ws, size_t ws_bytes, void* stream) {
   return block_forward(p, nullptr, x, w_router, router_bias, w_gate, w_up, w_down, ws_gate, ws_up, ws_down, scales, y,
                        topk_ids_out, topk_w_out, ws, ws_bytes, stream);
@@ -1596,7 +1615,7 @@ moe_status moe_layer_forward(const moe_problem* p, const void* x, const void* w_
 moe_status moe_block_forward(const moe_problem* p, const moe_block_options* opt, const void* x,
                              const void* w_router, const float* router_bias, const void* w_gate, const void* w_up,
                              const void* w_down, const void* ws_gate, const void* ws_up, const void* ws_down,
-                             const float* scales, void* y, int32_t* topk_ids_out, float* topk_w_out, void* ws,
+                             const void* scales, void* y, int32_t* topk_ids_out, float* topk_w_out, void* ws,
                              size_t ws_bytes, void* stream) {
   return block_forward(p, opt, x, w_router, router_bias, w_gate, w_up, w_down, ws_gate, ws_up, ws_down, scales, y,
                        topk_ids_out, topk_w_out, ws, ws_bytes, stream);
@@ -1665,6 +1684,231 @@ moe_status moe_ep_expand_ids(const int32_t* counts, int32_t G, int32_t E_local, 
 }
 
 }  // extern "C"
+
+// ============================================================== a few tokens, one kernel
+// Workspace of moe_decode_forward.
+struct DecodeLayout {
+  size_t bar = 0, logits = 0, xs = 0, xn = 0, gate = 0, h = 0, total = 0;
+  int splits = 1;
+};
+// Slices of d in the router's logits: enough (16 experts, slice) units to give
+// every SM one, each slice at least one 32-column chunk.  A fixed SM count keeps
+// the workspace size a pure function of the problem.
+static int decode_splits(const moe_problem& p) {
+  const int64_t tiles = cdiv(p.E, 16), chunks = cdiv(p.d, 32);
+  return (int)std::max<int64_t>(1, std::min<int64_t>({kTargetTiles / tiles, chunks, (int64_t)kDecodeMaxSplit}));
+}
+static DecodeLayout decode_layout(const moe_problem& p) {
+  DecodeLayout L;
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    size_t r = o;
+    o += align_up(std::max<size_t>(bytes, 1), 256);
+    return r;
+  };
+  L.splits = decode_splits(p);
+  L.bar = take(sizeof(unsigned));
+  L.logits = take((size_t)L.splits * p.T * p.E * 4);
+  L.xs = take((size_t)p.T * p.d * 2);
+  L.xn = take((size_t)p.T * p.d * 2);
+  L.gate = take((size_t)p.T * 4);
+  L.h = take((size_t)p.T * (p.k + 1) * ldh_of(p) * 2);
+  L.total = o;
+  return L;
+}
+static moe_status check_decode(const moe_problem* p) {
+  moe_status s = check(p);
+  if (s != MOE_OK) return s;
+  if (p->act_dtype != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "the few-token forward takes BF16 activations");
+  if (p->T > kDecodeMaxT)
+    return fail(MOE_ERR_UNSUPPORTED, "T = %lld > %d (use moe_layer_forward)", (long long)p->T, kDecodeMaxT);
+  return MOE_OK;
+}
+
+template <int W>
+static cudaError_t launch_decode(const DecodeArgs& a, int grid, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)kDecodeThreads);
+  cfg.dynamicSmemBytes = (size_t)decode_smem(a.T <= 8 ? 1 : 2);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeCooperative;  // the grid's barriers need every CTA resident
+  at[0].val.cooperative = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return a.T <= 8 ? cudaLaunchKernelEx(&cfg, k_decode<W, 1>, a) : cudaLaunchKernelEx(&cfg, k_decode<W, 2>, a);
+}
+
+extern "C" size_t moe_decode_workspace_size(const moe_problem* p) {
+  return check_decode(p) == MOE_OK ? decode_layout(*p).total : 0;
+}
+
+extern "C" moe_status moe_decode_forward(const moe_problem* p, const moe_block_options* opt, const void* x,
+                                         const void* w_router, const float* router_bias, const void* w_gate,
+                                         const void* w_up, const void* w_down, const void* ws_gate, const void* ws_up,
+                                         const void* ws_down, const void* scales, void* y, int32_t* topk_ids_out,
+                                         float* topk_w_out, void* ws, size_t ws_bytes, void* stream) {
+  NvtxRange nvtx_("moe_decode_forward");
+  moe_status s = check_decode(p);
+  if (s != MOE_OK) return s;
+  const void* norm_w = opt ? opt->norm_weight : nullptr;
+  const void* gate_w = opt ? opt->shared_gate : nullptr;
+  if (norm_w && !(opt->norm_eps >= 0.f && opt->norm_eps < 1e30f))
+    return fail(MOE_ERR_INVALID_ARG, "norm_eps must be finite and >= 0");
+  if (p->T == 0) {
+    g_launches = 0;
+    return MOE_OK;
+  }
+  NEED(x);
+  NEED(w_router);
+  MAYBE(router_bias);
+  NEED(y);
+  MAYBE(topk_ids_out);
+  MAYBE(topk_w_out);
+  MAYBE(norm_w);
+  MAYBE(gate_w);
+  NEED(ws);
+  ExpertWeights w{w_gate, w_up, w_down, ws_gate, ws_up, ws_down, scales};
+  if ((s = check_weights(*p, w)) != MOE_OK) return s;
+  const DecodeLayout L = decode_layout(*p);
+  if (ws_bytes < L.total)
+    return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", ws_bytes, L.total);
+  DeviceInfo* dev;
+  if ((s = device_info(&dev)) != MOE_OK) return s;
+  g_launches_pending = 0;
+  pdl_reset();
+  cudaStream_t st = (cudaStream_t)stream;
+  char* wsp = (char*)ws;
+  const void* xin = x;
+  float* gate = (gate_w && p->I_s > 0) ? (float*)(wsp + L.gate) : nullptr;
+  if (norm_w || gate) {
+    if ((s = launch_prologue(*p, x, norm_w, norm_w ? opt->norm_eps : 0.f, gate ? gate_w : nullptr, wsp + L.xn, gate,
+                             st)) != MOE_OK)
+      return s;
+    if (norm_w) xin = wsp + L.xn;
+  }
+  CUDA_TRY(cudaMemsetAsync(wsp + L.bar, 0, sizeof(unsigned), st));
+  pdl_reset();
+  DecodeArgs a{};
+  a.T = (int)p->T;
+  a.d = p->d;
+  a.E = p->E;
+  a.k = p->k;
+  a.I = p->I;
+  a.I_s = p->I_s;
+  a.x = (const bf16*)xin;
+  a.w_router = (const bf16*)w_router;
+  a.bias = router_bias;
+  a.wg = (const uint8_t*)w.wg;
+  a.wu = (const uint8_t*)w.wu;
+  a.wd = (const uint8_t*)w.wd;
+  a.sg = (const uint8_t*)w.sg;
+  a.su = (const uint8_t*)w.su;
+  a.sd = (const uint8_t*)w.sd;
+  const void* sp[6];
+  scale_parts(*p, w.scales, sp);
+  for (int i = 0; i < 6; ++i) a.sc[i] = (const uint8_t*)sp[i];
+  a.gate = gate;
+  a.xs = (bf16*)(wsp + L.xs);
+  a.logits = (float*)(wsp + L.logits);
+  a.splits = L.splits;
+  a.h = (bf16*)(wsp + L.h);
+  a.ldh = (int)ldh_of(*p);
+  a.ids = topk_ids_out;
+  a.tw = topk_w_out;
+  a.y = (bf16*)y;
+  a.bar = (unsigned*)(wsp + L.bar);
+  a.status = dev->status;
+  PROF_BEGIN("decode", st);
+  if (p->w_dtype == MOE_BF16) CUDA_TRY(launch_decode<kDecBf16>(a, dev->sms, st));
+  else if (p->w_dtype == MOE_FP8_E4M3_B128) CUDA_TRY(launch_decode<kDecFp8>(a, dev->sms, st));
+  else CUDA_TRY(launch_decode<kDecMx4>(a, dev->sms, st));
+  LAUNCH_CHECK("decode", st);
+  g_launches = g_launches_pending;
+  return MOE_OK;
+}
+
+// ============================================================== microscaled 4-bit matrices
+static moe_status check_mx4(int64_t batch, int64_t rows, int64_t cols) {
+  if (batch < 0 || rows < 0 || cols <= 0)
+    return fail(MOE_ERR_INVALID_ARG, "batch = %lld, rows = %lld, cols = %lld", (long long)batch, (long long)rows,
+                (long long)cols);
+  if (cols % 32) return fail(MOE_ERR_INVALID_ARG, "cols = %lld is not a multiple of 32", (long long)cols);
+  const int64_t lim = INT32_MAX;
+  if (batch > lim || rows > lim || cols > lim) return fail(MOE_ERR_UNSUPPORTED, "a size is above 2^31 - 1");
+  const int64_t per = cdiv(rows, kMxTile) * cdiv(cols, kMxTile);
+  if (per > lim || (batch > 0 && per > lim / batch))
+    return fail(MOE_ERR_UNSUPPORTED, "more than 2^31 - 1 scale tiles");
+  return MOE_OK;
+}
+
+extern "C" size_t moe_mx4_scale_bytes(int64_t batch, int64_t rows, int64_t cols) {
+  if (check_mx4(batch, rows, cols) != MOE_OK) return 0;
+  return (size_t)(batch * cdiv(rows, kMxTile) * cdiv(cols, kMxTile)) * kMxTileBytes;
+}
+
+extern "C" moe_status moe_mx4_quantize(const void* x, int32_t dtype, int64_t batch, int64_t rows, int64_t cols,
+                                       void* codes, void* scales, void* stream) {
+  NvtxRange nvtx_("moe_mx4_quantize");
+  moe_status s = check_mx4(batch, rows, cols);
+  if (s != MOE_OK) return s;
+  if (dtype != MOE_F32 && dtype != MOE_BF16)
+    return fail(MOE_ERR_INVALID_ARG, "type %d is not F32 or BF16", dtype);
+  if (batch == 0 || rows == 0) {
+    g_launches = 0;
+    return MOE_OK;
+  }
+  NEED(x);
+  NEED(codes);
+  NEED(scales);
+  g_launches_pending = 0;
+  pdl_reset();
+  cudaStream_t st = (cudaStream_t)stream;
+  const int64_t rt = cdiv(rows, kMxTile), ct = cdiv(cols, kMxTile);
+  const unsigned grid = (unsigned)(batch * rt * ct);
+  PROF_BEGIN("mx4_quantize", st);
+  if (dtype == MOE_F32)
+    CUDA_TRY(launch(k_mx4_quantize<float>, grid, 256, 0, st, (const float*)x, rows, cols, rt, ct, (uint32_t*)codes,
+                    (uint4*)scales));
+  else
+    CUDA_TRY(launch(k_mx4_quantize<bf16>, grid, 256, 0, st, (const bf16*)x, rows, cols, rt, ct, (uint32_t*)codes,
+                    (uint4*)scales));
+  LAUNCH_CHECK("mx4_quantize", st);
+  g_launches = g_launches_pending;
+  return MOE_OK;
+}
+
+extern "C" moe_status moe_mx4_dequantize(const void* codes, const void* scales, int64_t batch, int64_t rows,
+                                         int64_t cols, int32_t dtype, void* out, void* stream) {
+  NvtxRange nvtx_("moe_mx4_dequantize");
+  moe_status s = check_mx4(batch, rows, cols);
+  if (s != MOE_OK) return s;
+  if (dtype != MOE_F32 && dtype != MOE_BF16)
+    return fail(MOE_ERR_INVALID_ARG, "type %d is not F32 or BF16", dtype);
+  if (batch == 0 || rows == 0) {
+    g_launches = 0;
+    return MOE_OK;
+  }
+  NEED(codes);
+  NEED(scales);
+  NEED(out);
+  g_launches_pending = 0;
+  pdl_reset();
+  cudaStream_t st = (cudaStream_t)stream;
+  const int64_t rt = cdiv(rows, kMxTile), ct = cdiv(cols, kMxTile);
+  const unsigned grid = (unsigned)(batch * rt * ct);
+  PROF_BEGIN("mx4_dequantize", st);
+  if (dtype == MOE_F32)
+    CUDA_TRY(launch(k_mx4_dequantize<float>, grid, 256, 0, st, (const uint32_t*)codes, (const uint4*)scales, rows,
+                    cols, rt, ct, (float*)out));
+  else
+    CUDA_TRY(launch(k_mx4_dequantize<bf16>, grid, 256, 0, st, (const uint32_t*)codes, (const uint4*)scales, rows,
+                    cols, rt, ct, (bf16*)out));
+  LAUNCH_CHECK("mx4_dequantize", st);
+  g_launches = g_launches_pending;
+  return MOE_OK;
+}
 
 // ============================================================== router without a workspace
 // For callers that cannot allocate device memory themselves (see

@@ -3,7 +3,10 @@
 // could not meet a 1e-5 relative error) and any shape the tensor-core kernels
 // do not take.  All accumulate in fp32.
 #pragma once
+#include <type_traits>
+
 #include "common.cuh"
+#include "mx4.cuh"
 
 namespace moe {
 
@@ -18,8 +21,8 @@ template <typename TW>
 struct WeightSet {
   const TW* routed;       // [E, N_r, K_r]
   const TW* shared;       // [N_s, K_s]
-  const float* sc_routed; // E4M3 only: [E][N_r/128][K_r/128]
-  const float* sc_shared; // E4M3 only: [N_s/128][K_s/128]
+  const void* sc_routed;  // E4M3: fp32 [E][N_r/128][K_r/128]; mx4: scale tiles, the same blocks
+  const void* sc_shared;  // E4M3: fp32 [N_s/128][K_s/128]; mx4: scale tiles
 };
 
 template <typename TA, typename TW>
@@ -51,14 +54,21 @@ __device__ __forceinline__ float load_w<uint8_t>(const uint8_t* w, int64_t idx) 
 
 template <typename TW>
 __device__ __forceinline__ float weight_at(const WeightSet<TW>& ws, int g, int E, int N, int K, int n, int c) {
-  const TW* base = g < E ? ws.routed + (int64_t)g * N * K : ws.shared;
-  float v = load_w<TW>(base, (int64_t)n * K + c);
-  if (sizeof(TW) == 1) {
-    int kb = (K + 127) / 128;
-    const float* s = g < E ? ws.sc_routed + (int64_t)g * ((N + 127) / 128) * kb : ws.sc_shared;
-    v *= __ldg(s + (n / 128) * kb + c / 128);
+  if constexpr (std::is_same<TW, mx4>::value) {  // N and K are multiples of 128
+    const int64_t at = g < E ? (int64_t)g * N * K : 0;
+    const uint8_t* s = static_cast<const uint8_t*>(g < E ? ws.sc_routed : ws.sc_shared);
+    return mx4_value((g < E ? ws.routed : ws.shared) + at / 2, s + at / 32, n, c, K);
+  } else {
+    const TW* base = g < E ? ws.routed + (int64_t)g * N * K : ws.shared;
+    float v = load_w<TW>(base, (int64_t)n * K + c);
+    if (sizeof(TW) == 1) {
+      int kb = (K + 127) / 128;
+      const float* s = static_cast<const float*>(g < E ? ws.sc_routed : ws.sc_shared);
+      if (g < E) s += (int64_t)g * ((N + 127) / 128) * kb;
+      v *= __ldg(s + (n / 128) * kb + c / 128);
+    }
+    return v;
   }
-  return v;
 }
 
 template <typename TA, typename TW, int EPI>

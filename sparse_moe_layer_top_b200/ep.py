@@ -73,8 +73,8 @@ class EPMoELayer:
     """One rank's share of an expert-parallel MoE block.
 
     w_router [E, d] and the shared expert are full replicas; wg, wu [E_l, I, d]
-    and wd [E_l, d, I] are this rank's experts, E_l = E / world.  With E4M3
-    weights (w="fp8"), ``scales`` is this rank's packed block-scale buffer
+    and wd [E_l, d, I] are this rank's experts, E_l = E / world.  With E4M3 or 4-bit
+    weights (w="fp8", "mx4"), ``scales`` is this rank's packed block-scale buffer
     (``split_scales``).  ``ops`` is the namespace of stage calls (default: this
     package)."""
 
@@ -92,12 +92,13 @@ class EPMoELayer:
         self.E_l = E // world
         if wg.shape[0] != self.E_l or wu.shape[0] != self.E_l or wd.shape[0] != self.E_l:
             raise ValueError("rank weights must hold E / world = %d experts" % self.E_l)
-        if w == "fp8":
-            n = _scale_blocks(self.E_l, d, I, I_s)
+        if w in ("fp8", "mx4"):
+            n = _scale_blocks(self.E_l, d, I, I_s) * (_MX4_TILE if w == "mx4" else 1)
             if scales is None or scales.numel() != n:
-                raise ValueError("E4M3 weights need this rank's %d block scales (split_scales)" % n)
+                raise ValueError("%s weights need this rank's %d block scales (split_scales)"
+                                 % ("E4M3" if w == "fp8" else "4-bit", n))
         elif scales is not None:
-            raise ValueError("block scales are for E4M3 weights only")
+            raise ValueError("block scales are for E4M3 and 4-bit weights only")
         self.scales = scales
         self.w_router, self.bias = w_router, bias
         self.wg, self.wu, self.wd = wg, wu, wd
@@ -194,22 +195,27 @@ def split_experts(rank, world, wg, wu, wd):
     return wg[sl].contiguous(), wu[sl].contiguous(), wd[sl].contiguous()
 
 
+_MX4_TILE = 512  # scale bytes of a 128 x 128 block of 4-bit weights
+
+
 def _scale_blocks(E, d, I, I_s):
     """Length of the packed E4M3 scale buffer: gate, up and down of E experts,
-    then the shared expert's three, one scale per 128 x 128 block each."""
+    then the shared expert's three, one scale per 128 x 128 block each (4-bit
+    weights: one tile of scale bytes per block, in the same order)."""
     per = (I // 128) * (d // 128)
     return 3 * E * per + (3 * (I_s // 128) * (d // 128) if I_s > 0 else 0)
 
 
 def split_scales(rank, world, E, d, I, I_s, scales):
-    """This rank's packed E4M3 block scales from the whole block's buffer: the
-    gate, up and down scales of its experts, then the shared expert's
-    (replicated), in the same packed order as the whole buffer."""
-    if scales.numel() != _scale_blocks(E, d, I, I_s):
+    """This rank's packed block scales (E4M3: fp32; 4-bit: uint8) from the whole
+    block's buffer: the gate, up and down scales of its experts, then the shared
+    expert's (replicated), in the same packed order as the whole buffer."""
+    unit = _MX4_TILE if scales.dtype == torch.uint8 else 1
+    if scales.numel() != unit * _scale_blocks(E, d, I, I_s):
         raise ValueError("scales hold %d values, not the %d of the whole block"
-                         % (scales.numel(), _scale_blocks(E, d, I, I_s)))
+                         % (scales.numel(), unit * _scale_blocks(E, d, I, I_s)))
     E_l = E // world
-    per = (I // 128) * (d // 128)
+    per = (I // 128) * (d // 128) * unit
     lo, hi = rank * E_l * per, (rank + 1) * E_l * per
     flat = scales.reshape(-1)
     parts = [flat[m * E * per:(m + 1) * E * per][lo:hi] for m in range(3)] + [flat[3 * E * per:]]
