@@ -296,7 +296,9 @@ MOE_API moe_status moe_router_topk_static(const moe_problem* p, const void* x, c
  * expert_form: 0 SIMT kernels, 1 row-tiled tensor-core GEMMs, 2 weight-row
  * (swap-AB) GEMMs, 3 row-tiled GEMMs on CTA pairs, 4 split (CTA pairs for the
  * groups of 256 rows or more, weight-row GEMMs for the others), 5 GEMMs on CTA
- * pairs with the tokens as the MMA's N; router_selects: 1 when the
+ * pairs with the tokens as the MMA's N, 6 weight-row GEMMs on 4-bit weights
+ * (block-scaled tensor cores, bf16 rows split into two E4M3 planes);
+ * router_selects: 1 when the
  * router's GEMM selects the top k in its epilogue (bf16, E <= 256, at least
  * 16 tiles of 128 tokens), 0 for the split-K GEMM + top-k kernel or the SIMT
  * router; gathered: 1 when the gate/up GEMM reads its rows straight from x.
@@ -326,7 +328,10 @@ MOE_API moe_status moe_forward_plan(const moe_problem* p, int32_t* expert_form, 
  *     256, the count rounded up to 16) as its N (E4M3 weights take the form
  *     of 2).  Never chosen automatically: it measured no faster than 2 on
  *     the skewed prefill batch and than 4 on long groups.
- * 2 to 6 return MOE_ERR_UNSUPPORTED when the types do not allow them. */
+ * 2 to 6 return MOE_ERR_UNSUPPORTED when the types do not allow them.  MXFP4
+ * weights take one tensor-core form under 0 and 2 to 6; it wants every weight
+ * matrix 32-byte aligned (MOE_ERR_ALIGNMENT), and a row of activations holding
+ * an infinity or a NaN gives a row of NaN. */
 MOE_API moe_status moe_set_path(int path);
 
 /* Synchronously read and clear the device status word of the current device

@@ -457,7 +457,7 @@ def rmsnorm(prob, x, norm_weight, eps=1e-6, out=None, stream=None):
     return out
 
 
-EXPERT_FORMS = ("simt", "rows", "weight_rows", "cta_pairs", "split", "cta_pairs_tokens_n")
+EXPERT_FORMS = ("simt", "rows", "weight_rows", "cta_pairs", "split", "cta_pairs_tokens_n", "weight_rows_mx4")
 
 
 def forward_plan(prob):

@@ -22,6 +22,7 @@
 #include "router.cuh"
 #include "simt.cuh"
 #include "tc_gemm.cuh"
+#include "tc_mx4.cuh"
 #include "tc_swap.cuh"
 #include "tc_swap8.cuh"
 #include "tc_pair.cuh"
@@ -327,6 +328,9 @@ static moe_status device_info(DeviceInfo** out) {
     CUDA_TRY(allow_smem(k_gemm_swap8<true, kTcSwiGLU>, Swap8Cfg<true>::SMEM_BYTES));
     CUDA_TRY(allow_smem(k_gemm_swap8<true, kTcSlotStore>, Swap8Cfg<true>::SMEM_BYTES));
     CUDA_TRY(allow_smem(k_gemm_swap8<true, kTcStore>, Swap8Cfg<true>::SMEM_BYTES));
+    CUDA_TRY(allow_smem(k_gemm_mx4<kTcSwiGLU>, Mx4Cfg::SMEM_BYTES));
+    CUDA_TRY(allow_smem(k_gemm_mx4<kTcSlotStore>, Mx4Cfg::SMEM_BYTES));
+    CUDA_TRY(allow_smem(k_gemm_mx4<kTcStore>, Mx4Cfg::SMEM_BYTES));
     CUDA_TRY(allow_smem(k_decode<kDecBf16, 1>, decode_smem(1)));
     CUDA_TRY(allow_smem(k_decode<kDecBf16, 2>, decode_smem(2)));
     CUDA_TRY(allow_smem(k_decode<kDecFp8, 1>, decode_smem(1)));
@@ -395,6 +399,38 @@ static moe_status map3d(CUtensorMap* m, const void* base, uint64_t inner, uint64
   return map_tile(m, base, bytes, 3, dims, st, box_rows, wide);
 }
 
+// 4-bit weights [outer, rows, K]: box 128 codes x 128 rows, unpacked on the way
+// into 16 codes per 16 bytes (the MMA's 8-bit containers), 128-byte swizzle.
+static moe_status map_mx4(CUtensorMap* m, const void* base, int rank, uint64_t K, uint64_t rows, uint64_t outer) {
+  EncodeTiledFn enc;
+  moe_status s = encode_fn(&enc);
+  if (s != MOE_OK) return s;
+  cuuint64_t gd[3] = {K, rows, outer}, gs[2] = {K / 2, rows * K / 2};
+  cuuint32_t box[3] = {128, 128, 1}, es[3] = {1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, rank, const_cast<void*>(base), gd, gs, box, es,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) on 4-bit weights %llu x %llu", (int)r,
+                (unsigned long long)K, (unsigned long long)rows);
+  return MOE_OK;
+}
+// The two E4M3 planes [2, rows, ld] of the activations: box 128 x kNCH x 2.
+static moe_status map_planes(CUtensorMap* m, const void* base, uint64_t ld, uint64_t rows) {
+  EncodeTiledFn enc;
+  moe_status s = encode_fn(&enc);
+  if (s != MOE_OK) return s;
+  cuuint64_t gd[3] = {ld, rows, 2}, gs[2] = {ld, rows * ld};
+  cuuint32_t box[3] = {128, (cuuint32_t)kNCH, 2}, es[3] = {1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), gd, gs, box, es,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) on activation planes %llu x %llu", (int)r,
+                (unsigned long long)ld, (unsigned long long)rows);
+  return MOE_OK;
+}
+
 // ============================================================== checks
 static size_t esize(int dt) { return dt == MOE_F32 ? 4 : dt == MOE_BF16 ? 2 : 1; }
 static size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
@@ -438,9 +474,10 @@ static bool misaligned(const void* ptr) { return (reinterpret_cast<uintptr_t>(pt
     if ((ptr) && misaligned(ptr)) return fail(MOE_ERR_ALIGNMENT, "%s is not 16-byte aligned", #ptr); \
   } while (0)
 
-// Tensor-core expert kernels: bf16 activations; bf16 or E4M3 weights.
+// Tensor-core expert kernels: bf16 activations; bf16, E4M3 or 4-bit weights.
 static bool tc_shapes(const moe_problem& p) {
-  return p.act_dtype == MOE_BF16 && (p.w_dtype == MOE_BF16 || p.w_dtype == MOE_FP8_E4M3_B128);
+  return p.act_dtype == MOE_BF16 &&
+         (p.w_dtype == MOE_BF16 || p.w_dtype == MOE_FP8_E4M3_B128 || p.w_dtype == MOE_MXFP4_B32);
 }
 
 static moe_status choose(bool tc_possible, bool* use_tc) {
@@ -468,7 +505,7 @@ static moe_status choose(bool tc_possible, bool* use_tc) {
 // 256-row tiles waste little on group tails (measured: 12-15 % faster at 4096
 // rows per expert, even at 1024, slower on prefill-sized Zipf-skewed groups);
 // else the row-tiled form.
-enum { kFormSimt = 0, kFormRows = 1, kFormSwap = 2, kFormPair = 3, kFormSplit = 4, kFormPairT = 5 };
+enum { kFormSimt = 0, kFormRows = 1, kFormSwap = 2, kFormPair = 3, kFormSplit = 4, kFormPairT = 5, kFormMx4 = 6 };
 constexpr int kPairRowsPerExpert = 2048;
 constexpr int kSplitRows = 256;
 static moe_status choose_form(const moe_problem& p, int* form) {
@@ -476,6 +513,7 @@ static moe_status choose_form(const moe_problem& p, int* form) {
   moe_status s = choose(tc_shapes(p), &tc);
   if (s != MOE_OK) return s;
   if (!tc) *form = kFormSimt;
+  else if (p.w_dtype == MOE_MXFP4_B32) *form = kFormMx4;  // one form: weight rows as M, 64-token chunks as N
   else if (g_path == 2) *form = kFormRows;
   else if (g_path == 3) *form = kFormSwap;
   else if (g_path == 4) *form = p.w_dtype == MOE_BF16 ? kFormPair : kFormRows;
@@ -529,12 +567,15 @@ static size_t router_scratch_bytes(const moe_problem& p) {
 
 struct Layout {
   size_t counts = 0, pre_a = 0, pre_b = 0, part = 0, ids = 0, tw = 0, offs = 0, row_tok = 0, row_w = 0, pos = 0,
-         row_dst = 0, xp = 0, xn = 0, gate = 0, h = 0, total = 0;
+         row_dst = 0, xp = 0, xn = 0, gate = 0, h = 0, hl = 0, sf = 0, total = 0;
 };
 
 static int64_t rows_total(const moe_problem& p) { return p.T * p.k + (p.I_s > 0 ? p.T : 0); }
 static int64_t n_chunks(const moe_problem& p) { return std::max<int64_t>(1, cdiv(p.T, kChunkTokens)); }
 static int64_t ldh_of(const moe_problem& p) { return std::max(p.I, p.I_s); }
+
+// kNCH-row chunks the groups of the 4-bit form have at most.
+static int64_t mx4_chunks(const moe_problem& p) { return rows_total(p) / kNCH + p.E + 1; }
 
 // Workspace of moe_layer_forward (forward) or of the stage calls.  In the
 // forward, the dispatched rows x_perm and the weighted (token, slot) rows of
@@ -569,6 +610,13 @@ static Layout layout(const moe_problem& p, bool forward) {
     L.gate = take(p.T * 4);       // the shared expert's gate per token
   }
   L.h = take(Rp * ldh_of(p) * ab);
+  if (p.w_dtype == MOE_MXFP4_B32) {
+    // the activations' two E4M3 planes and their scale tiles, first of the
+    // dispatched rows, then of the SwiGLU activations
+    const int64_t w = std::max<int64_t>(p.d, ldh_of(p));
+    L.hl = take(2 * Rp * w);
+    L.sf = take(mx4_chunks(p) * (w / 128) * kMxTileBytes);
+  }
   L.total = o;
   return L;
 }
@@ -1233,9 +1281,129 @@ static moe_status split_gemms(const moe_problem& p, const void* xp, const int32_
   return swap_gemms_t<false>(p, xp, offs, w, sa, sb, H, o, st, dev, kPhaseDown);
 }
 
+// Column tiles of the 4-bit form: 128 features of gate and up, 256 outputs.
+static int mx4_tiles_a(int n) { return (int)cdiv(n, 128); }
+static int mx4_tiles_b(int n) { return (int)cdiv(n, 256); }
+
+// Expert GEMMs on 4-bit weights (tc_mx4.cuh): each projection splits its
+// activations into E4M3 planes first.  hl, sf: the workspace parts of layout().
+static moe_status mx4_gemms(const moe_problem& p, const void* xp, const int32_t* offs, const ExpertWeights& w,
+                            int32_t* pre_a, int32_t* pre_b, void* H, void* hl, void* sf, const DownOut& o,
+                            cudaStream_t st, DeviceInfo* dev, const GatherSrc& g) {
+  const int64_t Rp = rows_total(p), ldh = ldh_of(p);
+  const bool sh = p.I_s > 0;
+  const void* sp[6];
+  scale_parts(p, w.scales, sp);
+  moe_status s;
+  CUtensorMap xm, bR, bS, cR, cS;
+  // gate/up + SwiGLU
+  MxSplitArgs q{};
+  q.x = (const bf16*)(g.x ? g.x : xp);
+  q.row_tok = g.x ? g.row_tok : nullptr;
+  q.x_rows = p.T;
+  q.offs = offs;
+  q.prefix = pre_a;
+  q.E = p.E;
+  q.col_tiles = mx4_tiles_a(p.I);
+  q.max_chunk = (int)mx4_chunks(p) - 1;
+  q.rows_cap = Rp;
+  q.ld = p.d;
+  q.K_r = q.K_s = p.d;
+  q.hl = (uint8_t*)hl;
+  q.sf = (uint8_t*)sf;
+  q.status = dev->status;
+  PROF_BEGIN("mx4_split", st);
+  CUDA_TRY(launch(k_mx_split, (unsigned)Rp, 256, 0, st, q));
+  LAUNCH_CHECK("mx4_split", st);
+  if ((s = map_planes(&xm, hl, p.d, Rp)) != MOE_OK) return s;
+  if ((s = map_mx4(&bR, w.wg, 3, p.d, p.I, p.E)) != MOE_OK) return s;
+  if ((s = map_mx4(&cR, w.wu, 3, p.d, p.I, p.E)) != MOE_OK) return s;
+  bS = bR;
+  cS = cR;
+  if (sh) {
+    if ((s = map_mx4(&bS, w.sg, 2, p.d, p.I_s, 1)) != MOE_OK) return s;
+    if ((s = map_mx4(&cS, w.su, 2, p.d, p.I_s, 1)) != MOE_OK) return s;
+  }
+  Mx4Args a{};
+  a.g.offs = offs;
+  a.g.prefix = pre_a;
+  a.g.E = p.E;
+  a.g.rows_cap = Rp;
+  a.g.single_rows = -1;
+  a.g.N_r = p.I;
+  a.g.N_s = p.I_s;
+  a.g.K_r = a.g.K_s = p.d;
+  a.g.H = (bf16*)H;
+  a.g.ldh = ldh;
+  a.g.status = dev->status;
+  a.sb_r = (const uint8_t*)sp[0];
+  a.sb_s = (const uint8_t*)sp[3];
+  a.sc_r = (const uint8_t*)sp[1];
+  a.sc_s = (const uint8_t*)sp[4];
+  a.sf = (const uint8_t*)sf;
+  a.ld = p.d;
+  a.col_tiles = q.col_tiles;
+  a.max_chunk = q.max_chunk;
+  PROF_BEGIN("gemm_tc_swiglu", st);
+  CUDA_TRY(launch(k_gemm_mx4<kTcSwiGLU>, dev->sms, Mx4Cfg::THREADS, Mx4Cfg::SMEM_BYTES, st, xm, bR, bS, cR, cS, a));
+  LAUNCH_CHECK("gemm_tc_swiglu", st);
+  // down
+  q.x = (const bf16*)H;
+  q.row_tok = nullptr;
+  q.prefix = pre_b;
+  q.col_tiles = mx4_tiles_b(p.d);
+  q.ld = (int)ldh;
+  q.K_r = p.I;
+  q.K_s = p.I_s;
+  PROF_BEGIN("mx4_split", st);
+  CUDA_TRY(launch(k_mx_split, (unsigned)Rp, 256, 0, st, q));
+  LAUNCH_CHECK("mx4_split", st);
+  if ((s = map_planes(&xm, hl, ldh, Rp)) != MOE_OK) return s;
+  if ((s = map_mx4(&bR, w.wd, 3, p.I, p.d, p.E)) != MOE_OK) return s;
+  bS = bR;
+  if (sh && (s = map_mx4(&bS, w.sd, 2, p.I_s, p.d, 1)) != MOE_OK) return s;
+  Mx4Args b{};
+  b.g.offs = offs;
+  b.g.prefix = pre_b;
+  b.g.E = p.E;
+  b.g.rows_cap = Rp;
+  b.g.single_rows = -1;
+  b.g.N_r = b.g.N_s = p.d;
+  b.g.K_r = p.I;
+  b.g.K_s = p.I_s;
+  b.g.status = dev->status;
+  b.sb_r = b.sc_r = (const uint8_t*)sp[2];  // the second 128-row half of each 256-row tile is in the same matrix
+  b.sb_s = b.sc_s = (const uint8_t*)sp[5];
+  b.sf = (const uint8_t*)sf;
+  b.ld = (int)ldh;
+  b.col_tiles = q.col_tiles;
+  b.max_chunk = q.max_chunk;
+  if (o.ys) {
+    b.g.ys = (bf16*)o.ys;
+    b.g.ys_rows = p.T * (p.k + 1);
+    b.g.ldy = p.d;
+    b.g.row_dst = o.row_dst;
+    b.g.row_w = o.row_w;
+    PROF_BEGIN("gemm_tc_down", st);
+    CUDA_TRY(launch(k_gemm_mx4<kTcSlotStore>, dev->sms, Mx4Cfg::THREADS, Mx4Cfg::SMEM_BYTES, st, xm, bR, bS, bR, bS, b));
+    LAUNCH_CHECK("gemm_tc_down", st);
+  } else {
+    b.g.out = (bf16*)o.out;
+    b.g.ldo = p.d;
+    PROF_BEGIN("gemm_tc_store", st);
+    CUDA_TRY(launch(k_gemm_mx4<kTcStore>, dev->sms, Mx4Cfg::THREADS, Mx4Cfg::SMEM_BYTES, st, xm, bR, bS, bR, bS, b));
+    LAUNCH_CHECK("gemm_tc_store", st);
+  }
+  return MOE_OK;
+}
+
 static moe_status expert_gemms(const moe_problem& p, int form, const void* xp, const int32_t* offs,
-                               const ExpertWeights& w, int32_t* pre_a, int32_t* pre_b, void* H, const DownOut& o,
-                               cudaStream_t st, DeviceInfo* dev, const GatherSrc& g = GatherSrc{}) {
+                               const ExpertWeights& w, int32_t* pre_a, int32_t* pre_b, char* ws, const Layout& L,
+                               const DownOut& o, cudaStream_t st, DeviceInfo* dev,
+                               const GatherSrc& g = GatherSrc{}) {
+  void* H = ws + L.h;
+  if (form == kFormMx4)
+    return mx4_gemms(p, xp, offs, w, pre_a, pre_b, H, ws + L.hl, ws + L.sf, o, st, dev, g);
   if (form == kFormSwap) {
     if (p.w_dtype == MOE_FP8_E4M3_B128) return swap_gemms_t<true>(p, xp, offs, w, pre_a, pre_b, H, o, st, dev);
     return swap_gemms_t<false>(p, xp, offs, w, pre_a, pre_b, H, o, st, dev);
@@ -1260,6 +1428,9 @@ static void schedules(const moe_problem& p, int form, Schedule* sa, Schedule* sb
   } else if (form == kFormSwap) {  // (token chunk, 128 weight rows) tiles; E4M3 down: 256 rows
     *sa = Schedule{kNCH, 128, p.I, p.I_s, 0, 0, 0, 0};
     *sb = Schedule{kNCH, p.w_dtype == MOE_FP8_E4M3_B128 ? 256 : 128, p.d, p.d, 0, 0, 0, 0};
+  } else if (form == kFormMx4) {  // (token chunk, 128 features of gate and up / 256 outputs) tiles
+    *sa = Schedule{kNCH, 128, p.I, p.I_s, 0, 0, 0, 0};
+    *sb = Schedule{kNCH, 256, p.d, p.d, 0, 0, 0, 0};
   } else if (form == kFormSplit) {  // pair tiles for the large groups, weight-row tiles for the rest
     *sa = Schedule{kPairBM, 128, p.I, p.I_s, 0, kSplitRows - 1, kNCH, 128};
     *sb = Schedule{kPairBM, 256, p.d, p.d, 0, kSplitRows - 1, kNCH, 128};
@@ -1279,6 +1450,16 @@ static moe_status check_weights(const moe_problem& p, const ExpertWeights& w) {
     NEED(w.sd);
   }
   if (p.w_dtype == MOE_FP8_E4M3_B128 || p.w_dtype == MOE_MXFP4_B32) NEED(w.scales);
+  return MOE_OK;
+}
+
+// The 4-bit tensor-core form's unpacking loads want 32-byte aligned weights.
+static moe_status check_mx4_weights(const moe_problem& p, int form, const ExpertWeights& w) {
+  if (form != kFormMx4) return MOE_OK;
+  const void* m[6] = {w.wg, w.wu, w.wd, w.sg, w.su, w.sd};
+  for (int i = 0; i < (p.I_s > 0 ? 6 : 3); ++i)
+    if (reinterpret_cast<uintptr_t>(m[i]) & 31u)
+      return fail(MOE_ERR_ALIGNMENT, "4-bit weight matrix %d is not 32-byte aligned", i);
   return MOE_OK;
 }
 
@@ -1440,6 +1621,7 @@ moe_status moe_expert_ffn(const moe_problem* p, const void* x_perm, const int32_
     return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", ws_bytes, L.total);
   int form;
   if ((s = choose_form(*p, &form)) != MOE_OK) return s;
+  if ((s = check_mx4_weights(*p, form, w)) != MOE_OK) return s;
   DeviceInfo* dev;
   if ((s = device_info(&dev)) != MOE_OK) return s;
   g_launches_pending = 0;
@@ -1454,7 +1636,7 @@ moe_status moe_expert_ffn(const moe_problem* p, const void* x_perm, const int32_
   CUDA_TRY(launch(k_tile_prefix, 1, 1024, 0, st, offs, p->E, sa, pre_a, sb, pre_b));
   LAUNCH_CHECK("tile_prefix", st);
   DownOut o{nullptr, nullptr, nullptr, y_perm};
-  s = expert_gemms(*p, form, x_perm, offs, w, pre_a, pre_b, wsp + L.h, o, st, dev);
+  s = expert_gemms(*p, form, x_perm, offs, w, pre_a, pre_b, wsp, L, o, st, dev);
   if (s == MOE_OK) g_launches = g_launches_pending;
   return s;
 }
@@ -1538,6 +1720,7 @@ static moe_status block_forward(const moe_problem* p, const moe_block_options* o
     return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", ws_bytes, L.total);
   int form;
   if ((s = choose_form(*p, &form)) != MOE_OK) return s;
+  if ((s = check_mx4_weights(*p, form, w)) != MOE_OK) return s;
   DeviceInfo* dev;
   if ((s = device_info(&dev)) != MOE_OK) return s;
   g_launches_pending = 0;
@@ -1578,7 +1761,8 @@ static moe_status block_forward(const moe_problem* p, const moe_block_options* o
   // Measured: 35B shape (x 16 MB) 0.524 -> 0.484 ms; prefill (x 128 MB, in
   // the panel tile order) 10.80 -> 10.62 ms.
   GatherSrc gs;
-  if (gathers_rows(*p, form)) gs = GatherSrc{xin, row_tok};
+  // (the 4-bit form gathers in its split of the rows into E4M3 planes)
+  if (gathers_rows(*p, form) || form == kFormMx4) gs = GatherSrc{xin, row_tok};
   {
     NvtxRange r_("moe.dispatch");
     s = launch_dispatch(*p, ids, tw, counted, offs, row_tok, row_w, pos, row_dst, counts, sa, pre_a, sb, pre_b, xin,
@@ -1588,7 +1772,7 @@ static moe_status block_forward(const moe_problem* p, const moe_block_options* o
   DownOut o{xp, row_dst, row_w, nullptr};  // the slot rows reuse the dispatched-row buffer
   {
     NvtxRange r_("moe.expert_gemms");
-    s = expert_gemms(*p, form, xp, offs, w, pre_a, pre_b, wsp + L.h, o, st, dev, gs);
+    s = expert_gemms(*p, form, xp, offs, w, pre_a, pre_b, wsp, L, o, st, dev, gs);
   }
   if (s != MOE_OK) return s;
   NvtxRange r_sum_("moe.slot_sum");
