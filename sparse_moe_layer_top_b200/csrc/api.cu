@@ -415,18 +415,18 @@ static moe_status map_mx4(CUtensorMap* m, const void* base, int rank, uint64_t K
                 (unsigned long long)K, (unsigned long long)rows);
   return MOE_OK;
 }
-// The two E4M3 planes [2, rows, ld] of the activations: box 128 x kNCH x 2.
-static moe_status map_planes(CUtensorMap* m, const void* base, uint64_t ld, uint64_t rows) {
+// The activations' E4M3 rows [rows, ld]: box 128 columns x box_rows.
+static moe_status map_planes(CUtensorMap* m, const void* base, uint64_t ld, uint64_t rows, int box_rows) {
   EncodeTiledFn enc;
   moe_status s = encode_fn(&enc);
   if (s != MOE_OK) return s;
-  cuuint64_t gd[3] = {ld, rows, 2}, gs[2] = {ld, rows * ld};
-  cuuint32_t box[3] = {128, (cuuint32_t)kNCH, 2}, es[3] = {1, 1, 1};
-  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), gd, gs, box, es,
+  cuuint64_t gd[2] = {ld, rows}, gs[1] = {ld};
+  cuuint32_t box[2] = {128, (cuuint32_t)box_rows}, es[2] = {1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), gd, gs, box, es,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
-    return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) on activation planes %llu x %llu", (int)r,
+    return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) on activation rows %llu x %llu", (int)r,
                 (unsigned long long)ld, (unsigned long long)rows);
   return MOE_OK;
 }
@@ -567,7 +567,7 @@ static size_t router_scratch_bytes(const moe_problem& p) {
 
 struct Layout {
   size_t counts = 0, pre_a = 0, pre_b = 0, part = 0, ids = 0, tw = 0, offs = 0, row_tok = 0, row_w = 0, pos = 0,
-         row_dst = 0, xp = 0, xn = 0, gate = 0, h = 0, hl = 0, sf = 0, total = 0;
+         row_dst = 0, xp = 0, xn = 0, gate = 0, h = 0, hl = 0, sf = 0, sfh = 0, total = 0;
 };
 
 static int64_t rows_total(const moe_problem& p) { return p.T * p.k + (p.I_s > 0 ? p.T : 0); }
@@ -611,11 +611,11 @@ static Layout layout(const moe_problem& p, bool forward) {
   }
   L.h = take(Rp * ldh_of(p) * ab);
   if (p.w_dtype == MOE_MXFP4_B32) {
-    // the activations' two E4M3 planes and their scale tiles, first of the
-    // dispatched rows, then of the SwiGLU activations
-    const int64_t w = std::max<int64_t>(p.d, ldh_of(p));
-    L.hl = take(2 * Rp * w);
-    L.sf = take(mx4_chunks(p) * (w / 128) * kMxTileBytes);
+    // the dispatched rows as E4M3 terms and the scale tiles of those rows and of
+    // the SwiGLU activations (whose terms take the place of h: two bytes a value)
+    L.hl = take(2 * Rp * p.d);
+    L.sf = take(mx4_chunks(p) * (p.d / 128) * kMxTileBytes);
+    L.sfh = take(mx4_chunks(p) * (ldh_of(p) / 128) * kMxTileBytes);
   }
   L.total = o;
   return L;
@@ -1285,17 +1285,17 @@ static moe_status split_gemms(const moe_problem& p, const void* xp, const int32_
 static int mx4_tiles_a(int n) { return (int)cdiv(n, 128); }
 static int mx4_tiles_b(int n) { return (int)cdiv(n, 256); }
 
-// Expert GEMMs on 4-bit weights (tc_mx4.cuh): each projection splits its
-// activations into E4M3 planes first.  hl, sf: the workspace parts of layout().
+// Expert GEMMs on 4-bit weights (tc_mx4.cuh): the rows are split into E4M3 terms,
+// the gate/up product writes the SwiGLU activations split the same way.
 static moe_status mx4_gemms(const moe_problem& p, const void* xp, const int32_t* offs, const ExpertWeights& w,
-                            int32_t* pre_a, int32_t* pre_b, void* H, void* hl, void* sf, const DownOut& o,
+                            int32_t* pre_a, int32_t* pre_b, char* ws, const Layout& L, const DownOut& o,
                             cudaStream_t st, DeviceInfo* dev, const GatherSrc& g) {
   const int64_t Rp = rows_total(p), ldh = ldh_of(p);
   const bool sh = p.I_s > 0;
   const void* sp[6];
   scale_parts(p, w.scales, sp);
   moe_status s;
-  CUtensorMap xm, bR, bS, cR, cS;
+  CUtensorMap xm, xs, bR, bS, cR, cS;
   // gate/up + SwiGLU
   MxSplitArgs q{};
   q.x = (const bf16*)(g.x ? g.x : xp);
@@ -1306,16 +1306,16 @@ static moe_status mx4_gemms(const moe_problem& p, const void* xp, const int32_t*
   q.E = p.E;
   q.col_tiles = mx4_tiles_a(p.I);
   q.max_chunk = (int)mx4_chunks(p) - 1;
-  q.rows_cap = Rp;
-  q.ld = p.d;
-  q.K_r = q.K_s = p.d;
-  q.hl = (uint8_t*)hl;
-  q.sf = (uint8_t*)sf;
+  q.rows = Rp;
+  q.d = p.d;
+  q.hl = (uint8_t*)(ws + L.hl);
+  q.sf = (uint8_t*)(ws + L.sf);
   q.status = dev->status;
   PROF_BEGIN("mx4_split", st);
-  CUDA_TRY(launch(k_mx_split, (unsigned)Rp, 256, 0, st, q));
+  CUDA_TRY(launch(k_mx_split, (unsigned)cdiv(Rp, kMxSplitRows), 32 * kMxSplitRows, 0, st, q));
   LAUNCH_CHECK("mx4_split", st);
-  if ((s = map_planes(&xm, hl, p.d, Rp)) != MOE_OK) return s;
+  if ((s = map_planes(&xm, q.hl, p.d, 2 * Rp, 2 * kNCH)) != MOE_OK) return s;
+  if ((s = map_planes(&xs, q.hl, p.d, 2 * Rp, 2 * Mx4Cfg::SMALL)) != MOE_OK) return s;
   if ((s = map_mx4(&bR, w.wg, 3, p.d, p.I, p.E)) != MOE_OK) return s;
   if ((s = map_mx4(&cR, w.wu, 3, p.d, p.I, p.E)) != MOE_OK) return s;
   bS = bR;
@@ -1333,32 +1333,24 @@ static moe_status mx4_gemms(const moe_problem& p, const void* xp, const int32_t*
   a.g.N_r = p.I;
   a.g.N_s = p.I_s;
   a.g.K_r = a.g.K_s = p.d;
-  a.g.H = (bf16*)H;
   a.g.ldh = ldh;
   a.g.status = dev->status;
   a.sb_r = (const uint8_t*)sp[0];
   a.sb_s = (const uint8_t*)sp[3];
   a.sc_r = (const uint8_t*)sp[1];
   a.sc_s = (const uint8_t*)sp[4];
-  a.sf = (const uint8_t*)sf;
+  a.sf = q.sf;
   a.ld = p.d;
   a.col_tiles = q.col_tiles;
   a.max_chunk = q.max_chunk;
+  a.hl_out = (uint8_t*)(ws + L.h);
+  a.sf_out = (uint8_t*)(ws + L.sfh);
   PROF_BEGIN("gemm_tc_swiglu", st);
-  CUDA_TRY(launch(k_gemm_mx4<kTcSwiGLU>, dev->sms, Mx4Cfg::THREADS, Mx4Cfg::SMEM_BYTES, st, xm, bR, bS, cR, cS, a));
+  CUDA_TRY(launch(k_gemm_mx4<kTcSwiGLU>, dev->sms, Mx4Cfg::THREADS, Mx4Cfg::SMEM_BYTES, st, xm, xs, bR, bS, cR, cS, a));
   LAUNCH_CHECK("gemm_tc_swiglu", st);
   // down
-  q.x = (const bf16*)H;
-  q.row_tok = nullptr;
-  q.prefix = pre_b;
-  q.col_tiles = mx4_tiles_b(p.d);
-  q.ld = (int)ldh;
-  q.K_r = p.I;
-  q.K_s = p.I_s;
-  PROF_BEGIN("mx4_split", st);
-  CUDA_TRY(launch(k_mx_split, (unsigned)Rp, 256, 0, st, q));
-  LAUNCH_CHECK("mx4_split", st);
-  if ((s = map_planes(&xm, hl, ldh, Rp)) != MOE_OK) return s;
+  if ((s = map_planes(&xm, a.hl_out, ldh, 2 * Rp, 2 * kNCH)) != MOE_OK) return s;
+  if ((s = map_planes(&xs, a.hl_out, ldh, 2 * Rp, 2 * Mx4Cfg::SMALL)) != MOE_OK) return s;
   if ((s = map_mx4(&bR, w.wd, 3, p.I, p.d, p.E)) != MOE_OK) return s;
   bS = bR;
   if (sh && (s = map_mx4(&bS, w.sd, 2, p.I_s, p.d, 1)) != MOE_OK) return s;
@@ -1374,9 +1366,9 @@ static moe_status mx4_gemms(const moe_problem& p, const void* xp, const int32_t*
   b.g.status = dev->status;
   b.sb_r = b.sc_r = (const uint8_t*)sp[2];  // the second 128-row half of each 256-row tile is in the same matrix
   b.sb_s = b.sc_s = (const uint8_t*)sp[5];
-  b.sf = (const uint8_t*)sf;
+  b.sf = a.sf_out;
   b.ld = (int)ldh;
-  b.col_tiles = q.col_tiles;
+  b.col_tiles = mx4_tiles_b(p.d);
   b.max_chunk = q.max_chunk;
   if (o.ys) {
     b.g.ys = (bf16*)o.ys;
@@ -1385,13 +1377,14 @@ static moe_status mx4_gemms(const moe_problem& p, const void* xp, const int32_t*
     b.g.row_dst = o.row_dst;
     b.g.row_w = o.row_w;
     PROF_BEGIN("gemm_tc_down", st);
-    CUDA_TRY(launch(k_gemm_mx4<kTcSlotStore>, dev->sms, Mx4Cfg::THREADS, Mx4Cfg::SMEM_BYTES, st, xm, bR, bS, bR, bS, b));
+    CUDA_TRY(launch(k_gemm_mx4<kTcSlotStore>, dev->sms, Mx4Cfg::THREADS, Mx4Cfg::SMEM_BYTES, st, xm, xs, bR, bS, bR, bS,
+                    b));
     LAUNCH_CHECK("gemm_tc_down", st);
   } else {
     b.g.out = (bf16*)o.out;
     b.g.ldo = p.d;
     PROF_BEGIN("gemm_tc_store", st);
-    CUDA_TRY(launch(k_gemm_mx4<kTcStore>, dev->sms, Mx4Cfg::THREADS, Mx4Cfg::SMEM_BYTES, st, xm, bR, bS, bR, bS, b));
+    CUDA_TRY(launch(k_gemm_mx4<kTcStore>, dev->sms, Mx4Cfg::THREADS, Mx4Cfg::SMEM_BYTES, st, xm, xs, bR, bS, bR, bS, b));
     LAUNCH_CHECK("gemm_tc_store", st);
   }
   return MOE_OK;
@@ -1403,7 +1396,7 @@ static moe_status expert_gemms(const moe_problem& p, int form, const void* xp, c
                                const GatherSrc& g = GatherSrc{}) {
   void* H = ws + L.h;
   if (form == kFormMx4)
-    return mx4_gemms(p, xp, offs, w, pre_a, pre_b, H, ws + L.hl, ws + L.sf, o, st, dev, g);
+    return mx4_gemms(p, xp, offs, w, pre_a, pre_b, ws, L, o, st, dev, g);
   if (form == kFormSwap) {
     if (p.w_dtype == MOE_FP8_E4M3_B128) return swap_gemms_t<true>(p, xp, offs, w, pre_a, pre_b, H, o, st, dev);
     return swap_gemms_t<false>(p, xp, offs, w, pre_a, pre_b, H, o, st, dev);

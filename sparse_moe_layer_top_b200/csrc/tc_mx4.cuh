@@ -12,19 +12,25 @@
 // that is the work of one bf16 MMA (the 8-bit rate is twice as high), while HBM and
 // the shared-memory fill carry a quarter and a half of the bytes.
 //
-// The shape is the weight-row form of tc_swap.cuh: weight rows are the MMA's M,
-// up to kNCH tokens of a group its N; a tile is two 128-row weight matrices, gate
-// and up, or the two halves of 256 rows of the down matrix; the tile list and the
-// epilogue are the ones defined there.
+// The tokens are the MMA's M, the weights its N: A holds the 2 x 64 plane rows of a
+// chunk of kNCH = 64 tokens (row 2j the hi terms of token j, row 2j + 1 its lo terms),
+// B 256 weight rows (128 of gate, 128 of up; or 256 rows of the down matrix).  Shared
+// memory bounds the loop: per 32 columns A and B are read once (32 + 64 wavefronts of
+// 128 bytes) and filled once (32 + 64), against 128 cycles of MMA.  The form with the
+// weights as M and 64 tokens as N, a separate MMA per plane and matrix, reads 192
+// and measured 3.32 ms on the gate/up product of 2048 tokens x 10 experts at
+// d = 8192, I = 2048, E = 512.
 // A K block is 128 columns: TMA unpacks the 4-bit rows into the 8-bit containers the
-// MMA reads (16 codes per 16 bytes, 128-byte swizzle), brings both planes of the
-// token tile in one box, and the scale tiles of the weights (one 512-byte tile per
-// matrix: their layout in memory is the tensor core's) and of the tokens as plain
-// bulk copies.  The MMA thread moves the scale tiles into TMEM
-// (tcgen05.cp.32x128b.warpx4) ahead of the MMAs that read them.
+// MMA reads (16 codes per 16 bytes, 128-byte swizzle), and the scale tiles of the
+// weights (one 512-byte tile per 128 rows: their layout in memory is the tensor core's)
+// and of the tokens come as plain bulk copies.  The MMA thread moves the scale tiles
+// into TMEM (tcgen05.cp.32x128b.warpx4) ahead of the MMAs that read them.
 //
-// TMEM: two accumulator buffers of 2 kNCH columns, then 16 scale columns per
-// stage (gate 4, up 4, tokens 4: rows 0..63 of the hi plane, then of the lo plane).
+// The tile list is the one of tc_swap.cuh: the chunks of one weight tile are adjacent.
+// TMEM: one accumulator of 256 columns, then 16 scale columns per stage (tokens 4,
+// weights 8).  Two accumulators and the scales do not fit 512 columns; the epilogue
+// warps instead take the whole accumulator into registers (128 a thread) and hand it
+// back before they compute or store, while the loads run on.
 //
 // Warps: 0 producer; 1 TMEM owner and MMA issuer; 2..9 epilogue.
 #pragma once
@@ -36,40 +42,41 @@ namespace moe {
 enum : unsigned { kKernGemmMx4 = 5 };
 
 struct Mx4Cfg {
-  static constexpr int KB = 128;                   // columns per K block
-  static constexpr int W_BYTES = 128 * KB;         // one matrix, unpacked
-  static constexpr int X_BYTES = 2 * kNCH * KB;    // hi and lo planes
-  static constexpr int SF_AT = 2 * W_BYTES + X_BYTES;
-  // bytes the barrier counts: the unpacking load counts the packed codes it reads
-  static constexpr int TX_BYTES = 2 * (W_BYTES / 2) + X_BYTES + 3 * kMxTileBytes;
+  static constexpr int KB = 128;                 // columns per K block
+  static constexpr int A_BYTES = 2 * kNCH * KB;  // hi and lo rows of the token chunk
+  static constexpr int B_BYTES = 256 * KB;       // weight rows, unpacked
+  static constexpr int SF_AT = A_BYTES + B_BYTES;
   static constexpr int STAGE_BYTES = (SF_AT + 3 * kMxTileBytes + 1023) / 1024 * 1024;
+  static constexpr int SMALL = 16;               // chunks of at most this many tokens load 2 * SMALL rows of A
+  // bytes the barrier counts: the unpacking loads count the packed codes they read
+  static constexpr int TX_BYTES = A_BYTES + B_BYTES / 2 + 3 * kMxTileBytes;
+  static constexpr int TX_SMALL = TX_BYTES - A_BYTES + 2 * SMALL * KB;
   static constexpr int STAGES = 4;
   static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
   static constexpr int EPI_WARPS = 8;
   static constexpr int THREADS = 64 + 32 * EPI_WARPS;
-  static constexpr int ACC_COLS = 2 * kNCH;
-  static constexpr int SF_COL = 2 * ACC_COLS, SF_COLS = 16;
+  static constexpr int SF_COL = 256, SF_COLS = 16;
   static constexpr int TMEM_COLS = 512;
-  static constexpr int BAR_BYTES = (2 * STAGES + 5) * 8 + 16;
+  static constexpr int BAR_BYTES = (2 * STAGES + 3) * 8 + 8;
   static constexpr int SCHED_INTS = 2 * (512 + 2);
   static constexpr int SMEM_BYTES = 1024 + RING_BYTES + BAR_BYTES + SCHED_INTS * 4;
   static_assert(SF_COL + STAGES * SF_COLS <= TMEM_COLS, "TMEM columns");
-  static_assert(W_BYTES % 1024 == 0 && X_BYTES % 1024 == 0, "swizzled tiles need 1024-byte alignment");
+  static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0, "swizzled tiles need 1024-byte alignment");
   static_assert(SMEM_BYTES <= 232448, "shared memory");
 };
 
 // ---------------------------------------------------------------- activations
-// Row r of the activations (row_tok ? x[row_tok[r]] : x[r], ld elements wide, the
-// first K_r or K_s of them used) as two E4M3 planes hl[2][rows_cap][ld] and
-// scale tiles sf[chunk][ld / 128][512], chunk = the kNCH-row chunk of the row's
-// group, numbered over the groups as the GEMM's tile list numbers them
-// (prefix[g] / col_tiles; prefix of the routed groups' column tiles).  Rows in
-// no group are left alone.
+// Row r of the activations (row_tok ? x[row_tok[r]] : x[r], d elements) as two
+// rows of E4M3 terms, hl[2 r] (hi) and hl[2 r + 1] (lo), and scale tiles
+// sf[chunk][d / 128][512], chunk = the kNCH-row chunk of the row's group,
+// numbered over the groups as the GEMM's tile list numbers them (prefix[g] /
+// col_tiles; prefix of the routed groups' column tiles), tile rows as the MMA's A
+// rows.  Rows in no group are left alone.
 //
 // Scale: the power of two that puts the block's largest value in (224, 448], the
 // top of E4M3's range; at least 2^-123, so that lo's byte (four less) exists.  A
 // block holding an infinity or a NaN becomes NaN.
-// One block of 256 threads per row, 8 values a thread, 4 threads a scale block.
+// One warp per row, 8 values a lane (4 lanes a scale block), four loads in flight.
 struct MxSplitArgs {
   const bf16* x;
   const int32_t* row_tok;  // NULL: row r itself
@@ -77,12 +84,13 @@ struct MxSplitArgs {
   const int32_t* prefix;
   int E, col_tiles;
   int max_chunk;           // last chunk the scale buffer holds
-  int64_t rows_cap, x_rows;
-  int ld, K_r, K_s;
+  int64_t rows, x_rows;
+  int d;
   uint8_t* hl;
   uint8_t* sf;
   unsigned* status;
 };
+constexpr int kMxSplitRows = 8;  // rows per block, one warp each
 
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {  // a in the low byte
   uint16_t r;
@@ -94,83 +102,90 @@ __device__ __forceinline__ float2 e4m3x2_value(uint32_t q) {
   return __half22float2(__half2(h));
 }
 
-__global__ void __launch_bounds__(256) k_mx_split(MxSplitArgs p) {
+// Scale byte of a 32-value block whose largest magnitude has the bits amax:
+// amax = m * 2^(e - 127), and m <= 1.75 fits 448 = 1.75 * 2^8 under 2^(e - 127 - 8).
+__device__ __forceinline__ uint32_t mx_split_byte(uint32_t amax) {
+  const uint32_t e = amax >> 23;
+  if (e == 255u) return 255u;
+  const uint32_t b = e + ((amax & 0x7fffffu) > 0x600000u ? 1u : 0u);
+  return b < 12u ? 4u : b - 8u;
+}
+__device__ __forceinline__ uint32_t mx_lo_byte(uint32_t b) { return b == 255u ? 255u : b - 4u; }
+// Two values under scale byte b -> their hi codes (low half) and lo codes (high half).
+__device__ __forceinline__ uint32_t mx_split2(float v0, float v1, float inv) {
+  const float a0 = v0 * inv, a1 = v1 * inv;
+  const uint32_t h = e4m3x2(a0, a1);
+  const float2 w = e4m3x2_value(h);
+  return h | e4m3x2((a0 - w.x) * 16.f, (a1 - w.y) * 16.f) << 16;
+}
+__device__ __forceinline__ float mx_split_inv(uint32_t b) {  // a NaN block multiplies by NaN: codes of NaN
+  return b == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float((254u - b) << 23);
+}
+
+__global__ void __launch_bounds__(32 * kMxSplitRows) k_mx_split(MxSplitArgs p) {
   pdl_begin();  // after the previous kernel in the stream (programmatic launch)
-  const int64_t r = blockIdx.x;
-  if (r < __ldg(p.offs) || r >= __ldg(p.offs + p.E + 1)) return;
-  int lo = 0, hi = p.E + 1;  // offs[lo] <= r < offs[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(p.offs + mid) <= r) lo = mid; else hi = mid;
-  }
-  const int g = lo, j = (int)(r - __ldg(p.offs + g));
-  const int K = g < p.E ? p.K_r : p.K_s;
+  const int64_t r = (int64_t)blockIdx.x * kMxSplitRows + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (r >= p.rows || r < __ldg(p.offs) || r >= __ldg(p.offs + p.E + 1)) return;
+  // the row's group: the last g with offs[g] <= r, 32 candidates a step
+  const int step = (p.E + 32) / 32;  // E + 1 groups
+  const int g0 = (__popc(__ballot_sync(0xffffffffu, lane * step <= p.E && __ldg(p.offs + min(lane * step, p.E)) <= r)) - 1) * step;
+  const int g = g0 + __popc(__ballot_sync(0xffffffffu, lane < step && g0 + lane <= p.E && __ldg(p.offs + min(g0 + lane, p.E)) <= r)) - 1;
+  const int j = (int)(r - __ldg(p.offs + g));
   const int64_t chunk = __ldg(p.prefix + g) / p.col_tiles + j / kNCH;
-  if (chunk > p.max_chunk) return;  // group offsets that claim more rows than there are
-  const int jj = j % kNCH;
+  if (j < 0 || chunk > p.max_chunk) return;  // group offsets that claim more rows than there are
+  const int i = 2 * (j % kNCH);  // the MMA's A row of the hi terms
   int64_t src = r;
   if (p.row_tok) {
     src = __ldg(p.row_tok + r);
     if (!in_range(src, p.x_rows, p.status, kSiteGatherToken)) return;
   }
-  const bf16* x = p.x + src * p.ld;
-  uint8_t* hrow = p.hl + r * p.ld;
-  uint8_t* lrow = hrow + p.rows_cap * p.ld;
-  uint8_t* sf = p.sf + chunk * (p.ld / 128) * kMxTileBytes + (jj & 31) * 16 + (jj >> 5) * 4;
-  const int lane = threadIdx.x & 31;
-  for (int c0 = 0; c0 < K; c0 += 256 * 8) {  // uniform: K is a multiple of 128, a warp's 256 columns may end half way
-    const int c = c0 + threadIdx.x * 8;
-    const bool ok = c < K;
-    float v[8];
-    if (ok) {
-      load8<bf16>(x + c, v);
-    } else {
+  const bf16* x = p.x + src * p.d;
+  uint8_t* hrow = p.hl + 2 * r * p.d;
+  uint8_t* lrow = hrow + p.d;
+  uint8_t* sf = p.sf + chunk * (p.d / 128) * kMxTileBytes + (i & 31) * 16 + (i >> 5) * 4;
+  constexpr int U = 4;
+  for (int c0 = lane * 8; c0 < p.d; c0 += U * 256) {  // d is a multiple of 128: half warps agree
+    uint4 q[U];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    }
-    uint32_t amax = 0;
+    for (int u = 0; u < U; ++u)
+      q[u] = c0 + u * 256 < p.d ? __ldg(reinterpret_cast<const uint4*>(x + c0 + u * 256)) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);
-    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    // amax = m * 2^(e - 127): m <= 1.75 fits 448 = 1.75 * 2^8 under 2^(e - 127 - 8)
-    const uint32_t e = amax >> 23;
-    uint32_t b = e + ((amax & 0x7fffffu) > 0x600000u ? 1u : 0u);
-    b = b < 12u ? 4u : b - 8u;
-    const bool bad = e == 255u;
-    const float inv = __uint_as_float((254u - b) << 23);
-    uint32_t h[4], l[4];
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + u * 256;
+      if (c >= p.d) break;
+      const unsigned half = 0xffffu << (lane & 16);
+      const uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+      uint32_t amax = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a0 = v[2 * i] * inv, a1 = v[2 * i + 1] * inv;
-      h[i] = e4m3x2(a0, a1);
-      const float2 w = e4m3x2_value(h[i]);
-      l[i] = e4m3x2((a0 - w.x) * 16.f, (a1 - w.y) * 16.f);
-      if (bad) h[i] = l[i] = 0x7f7fu;
-    }
-    if (bad) b = 255u;
-    if (ok) {
-      *reinterpret_cast<uint2*>(hrow + c) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
-      *reinterpret_cast<uint2*>(lrow + c) = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
-    }
-    // the four bytes of a 128-column block meet in its first lane
-    const int base = lane & 16;
-    const uint32_t b1 = __shfl_sync(0xffffffffu, b, base + 4), b2 = __shfl_sync(0xffffffffu, b, base + 8),
-                   b3 = __shfl_sync(0xffffffffu, b, base + 12);
-    if ((lane & 15) == 0 && ok) {
-      uint8_t* d = sf + (int64_t)(c >> 7) * kMxTileBytes;
-      const uint32_t w = b | b1 << 8 | b2 << 16 | b3 << 24;
-      const uint32_t lw = (b == 255u ? b : b - 4u) | (b1 == 255u ? b1 : b1 - 4u) << 8 |
-                          (b2 == 255u ? b2 : b2 - 4u) << 16 | (b3 == 255u ? b3 : b3 - 4u) << 24;
-      *reinterpret_cast<uint32_t*>(d) = w;       // hi plane: rows 0..63 of the tile
-      *reinterpret_cast<uint32_t*>(d + 8) = lw;  // lo plane: rows 64..127
+      for (int t = 0; t < 4; ++t) amax = max(amax, max(w[t] << 16 & 0x7fff0000u, w[t] & 0x7fff0000u));
+      amax = max(amax, __shfl_xor_sync(half, amax, 1));
+      amax = max(amax, __shfl_xor_sync(half, amax, 2));
+      const uint32_t b = mx_split_byte(amax);
+      const float inv = mx_split_inv(b);
+      uint32_t s[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        s[t] = mx_split2(__uint_as_float(w[t] << 16), __uint_as_float(w[t] & 0xffff0000u), inv);
+      *reinterpret_cast<uint2*>(hrow + c) = make_uint2(__byte_perm(s[0], s[1], 0x5410), __byte_perm(s[2], s[3], 0x5410));
+      *reinterpret_cast<uint2*>(lrow + c) = make_uint2(__byte_perm(s[0], s[1], 0x7632), __byte_perm(s[2], s[3], 0x7632));
+      // the four bytes of a 128-column block meet in its first lane
+      const int base = lane & 16;
+      const uint32_t b1 = __shfl_sync(half, b, base + 4), b2 = __shfl_sync(half, b, base + 8),
+                     b3 = __shfl_sync(half, b, base + 12);
+      if ((lane & 15) == 0) {
+        uint8_t* t = sf + (int64_t)(c >> 7) * kMxTileBytes;
+        *reinterpret_cast<uint32_t*>(t) = b | b1 << 8 | b2 << 16 | b3 << 24;
+        *reinterpret_cast<uint32_t*>(t + 16) =
+            mx_lo_byte(b) | mx_lo_byte(b1) << 8 | mx_lo_byte(b2) << 16 | mx_lo_byte(b3) << 24;
+      }
     }
   }
 }
 
 // ---------------------------------------------------------------- PTX
-// D[tmem] (+)= (A * scale_A) (B * scale_B)^T: A 4-bit (E2M1 in 8-bit containers),
-// B E4M3, one scale byte per row and 32 columns from TMEM, fp32 accumulate.
+// D[tmem] (+)= (A * scale_A) (B * scale_B)^T: A E4M3, B 4-bit (E2M1 in 8-bit
+// containers), one scale byte per row and 32 columns from TMEM, fp32 accumulate.
 __device__ __forceinline__ void umma_mxf8f6f4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                               uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
   asm volatile(
@@ -195,10 +210,10 @@ __device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
   d |= (uint64_t)1 << 46;
   return d;
 }
-// Instruction descriptor, .kind::mxf8f6f4: A E2M1, B E4M3, both K-major, UE8M0
-// scales; `id` selects the byte of each scale word (the 32-column step).
+// Instruction descriptor, .kind::mxf8f6f4: A E4M3, B E2M1, both K-major, M = 128,
+// UE8M0 scales; `id` selects the byte of each scale word (the 32-column step).
 __device__ __forceinline__ uint32_t idesc_mx4(int N, int id) {
-  return ((uint32_t)id << 4) | (5u << 7) | (0u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | (1u << 27) |
+  return ((uint32_t)id << 4) | (0u << 7) | (5u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | (1u << 27) |
          ((uint32_t)id << 29);
 }
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t policy) {
@@ -209,22 +224,42 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
-// tmX: token planes (box 128 x kNCH x 2); tmB / tmC: 4-bit weight maps (box 128
-// codes x 128 rows), gate (or the down matrix) and up; _r [E, N, K], _s [N, K].
+// The accumulator's hi rows (even lanes) and lo rows (odd lanes) of 64 columns
+// (a: 0..31, b: 32..63) summed: the even lane gets columns 0..31 in a, the odd
+// lane 32..63.
+__device__ __forceinline__ void mx_sum_planes(uint32_t (&a)[32], const uint32_t (&b)[32], bool odd) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? a[j] : b[j], 1);
+    a[j] = __float_as_uint(__uint_as_float(odd ? b[j] : a[j]) + __uint_as_float(got));
+  }
+}
+__device__ __forceinline__ uint4 mx_bf16x8(const uint32_t* v, float w) {
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = pack_bf16x2(w * __uint_as_float(v[2 * i]), w * __uint_as_float(v[2 * i + 1]));
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// tmX / tmXs: the hi / lo rows (box 128 columns x 128 rows / 2 * SMALL rows);
+// tmB / tmC: 4-bit weight maps (box 128 codes x 128 rows), gate (or the down
+// matrix) and up; _r [E, N, K], _s [N, K].
 struct Mx4Args {
   TcGemmArgs g;
   const uint8_t *sb_r, *sb_s, *sc_r, *sc_s;  // weight scale tiles of B and C
   const uint8_t* sf;                         // token scale tiles
-  int ld;                                    // columns of the token planes
+  int ld;                                    // columns of the token rows
   int col_tiles;                             // column tiles of a routed group
-  int max_chunk;                             // last chunk sf holds
+  int max_chunk;                             // last chunk sf (and sf_out) holds
+  uint8_t* hl_out;                           // SwiGLU: the activations as hi / lo rows of ldh columns
+  uint8_t* sf_out;                           // and their scale tiles
 };
 
 template <int EPI>
 __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
-    k_gemm_mx4(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmB_r,
-               const __grid_constant__ CUtensorMap tmB_s, const __grid_constant__ CUtensorMap tmC_r,
-               const __grid_constant__ CUtensorMap tmC_s, Mx4Args a) {
+    k_gemm_mx4(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXs,
+               const __grid_constant__ CUtensorMap tmB_r, const __grid_constant__ CUtensorMap tmB_s,
+               const __grid_constant__ CUtensorMap tmC_r, const __grid_constant__ CUtensorMap tmC_s, Mx4Args a) {
   using Cfg = Mx4Cfg;
   constexpr int S = Cfg::STAGES;
   constexpr bool HALVES = EPI != kTcSwiGLU;  // two halves of 256 rows of one matrix
@@ -236,8 +271,8 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::RING_BYTES);
   uint64_t* empty = full + S;
   uint64_t* tfull = empty + S;
-  uint64_t* tempty = tfull + 2;
-  uint64_t* drain = tempty + 2;
+  uint64_t* tempty = tfull + 1;
+  uint64_t* drain = tempty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int32_t* s_pre = reinterpret_cast<int32_t*>(smem + Cfg::RING_BYTES + Cfg::BAR_BYTES);
@@ -250,16 +285,15 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
       mbar_init(full + s, 1);
       mbar_init(empty + s, 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(tfull + b, 1);
-      mbar_init(tempty + b, Cfg::EPI_WARPS);
-    }
+    mbar_init(tfull, 1);
+    mbar_init(tempty, Cfg::EPI_WARPS);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&tmX);
+    prefetch_tmap(&tmXs);
     prefetch_tmap(&tmB_r);
     prefetch_tmap(&tmB_s);
     prefetch_tmap(&tmC_r);
@@ -269,7 +303,7 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
     tmem_alloc(tmem_slot, Cfg::TMEM_COLS);
     tmem_relinquish();
   }
-  pdl_begin();  // the schedule and the token planes come from earlier kernels
+  pdl_begin();  // the schedule and the token rows come from earlier kernels
   for (int i = threadIdx.x; i < p.E + 2; i += blockDim.x) {
     s_pre[i] = __ldg(p.prefix + i);
     s_offs[i] = __ldg(p.offs + i);
@@ -293,9 +327,10 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
         const bool sh = t.g == p.E;
         const int nkb = (sh ? p.K_s : p.K_r) / Cfg::KB;
         // scale tiles: [group][row tile][K block]; a second half past the matrix
-        // re-reads the first half's (its codes read as zero and its rows are not stored)
+        // re-reads the first half's (neither it nor its codes are multiplied)
         const int64_t rt = (int64_t)(sh ? 0 : t.g) * (t.N / 128) + t.n0 / 128;
         const bool c_in = t.n0 + C_ROW < t.N;
+        const bool small = t.rows - t.c0 <= Cfg::SMALL;
         const uint8_t* sb = (sh ? a.sb_s : a.sb_r) + rt * nkb * kMxTileBytes;
         const uint8_t* sc = (sh ? a.sc_s : a.sc_r) + (rt + (c_in ? C_ROW / 128 : 0)) * nkb * kMxTileBytes;
         const uint8_t* sx =
@@ -307,19 +342,21 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
           }
           uint64_t* land = full + stage;
           uint8_t* base = smem + stage * Cfg::STAGE_BYTES;
+          uint8_t* wb = base + Cfg::A_BYTES;
+          uint8_t* sf = base + Cfg::SF_AT;
           const int k0 = kb * Cfg::KB;
-          mbar_arrive_expect_tx(land, Cfg::TX_BYTES);
+          mbar_arrive_expect_tx(land, small ? Cfg::TX_SMALL : Cfg::TX_BYTES);
           if (sh) {
-            tma_load_2d(base, &tmB_s, land, k0, t.n0, pol_w);
-            tma_load_2d(base + Cfg::W_BYTES, &tmC_s, land, k0, t.n0 + C_ROW, pol_w);
+            tma_load_2d(wb, &tmB_s, land, k0, t.n0, pol_w);
+            tma_load_2d(wb + Cfg::B_BYTES / 2, &tmC_s, land, k0, t.n0 + C_ROW, pol_w);
           } else {
-            tma_load_3d(base, &tmB_r, land, k0, t.n0, t.g, pol_w);
-            tma_load_3d(base + Cfg::W_BYTES, &tmC_r, land, k0, t.n0 + C_ROW, t.g, pol_w);
+            tma_load_3d(wb, &tmB_r, land, k0, t.n0, t.g, pol_w);
+            tma_load_3d(wb + Cfg::B_BYTES / 2, &tmC_r, land, k0, t.n0 + C_ROW, t.g, pol_w);
           }
-          tma_load_3d(base + 2 * Cfg::W_BYTES, &tmX, land, k0, (int)t.row0, 0, pol_x);
-          bulk_load(base + Cfg::SF_AT, sb + (int64_t)kb * kMxTileBytes, kMxTileBytes, land, pol_w);
-          bulk_load(base + Cfg::SF_AT + kMxTileBytes, sc + (int64_t)kb * kMxTileBytes, kMxTileBytes, land, pol_w);
-          bulk_load(base + Cfg::SF_AT + 2 * kMxTileBytes, sx + (int64_t)kb * kMxTileBytes, kMxTileBytes, land, pol_x);
+          tma_load_2d(base, small ? &tmXs : &tmX, land, k0, 2 * (int)t.row0, pol_x);
+          bulk_load(sf, sx + (int64_t)kb * kMxTileBytes, kMxTileBytes, land, pol_x);
+          bulk_load(sf + kMxTileBytes, sb + (int64_t)kb * kMxTileBytes, kMxTileBytes, land, pol_w);
+          bulk_load(sf + 2 * kMxTileBytes, sc + (int64_t)kb * kMxTileBytes, kMxTileBytes, land, pol_w);
           issued |= 1u << stage;
           last_par = (last_par & ~(1u << stage)) | (phase << stage);
           if (++stage == S) {
@@ -336,39 +373,32 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
   } else if (warp == 1) {
     if (lane == 0) {
       // ------------------------------------------------ MMA issuer
-      int stage = 0, acc = 0;
+      int stage = 0;
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
         const SwapTile t = decode_swap<TILE_ROWS>(p, s_pre, s_offs, tile);
-        const int n = min(kNCH, (t.rows - t.c0 + 15) & ~15);  // the MMA's N: the chunk's tokens rounded up to 16
+        const int n = t.n0 + C_ROW < t.N ? 256 : 128;  // weight rows that exist
         const int nkb = (t.g == p.E ? p.K_s : p.K_r) / Cfg::KB;
-        if (!mbar_wait(tempty + acc, acc_phase ^ 1, abort_flag, p.status, tcode | 2)) break;
+        if (!mbar_wait(tempty, acc_phase ^ 1, abort_flag, p.status, tcode | 2)) break;
         tc_fence_after();
-        const uint32_t d0 = tmem_base + acc * Cfg::ACC_COLS;
         for (int kb = 0; kb < nkb; ++kb) {
           if (!mbar_wait(full + stage, phase, abort_flag, p.status, tcode | 3)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sw = smem_u32(smem + stage * Cfg::STAGE_BYTES);
-          const uint32_t sx = sw + 2 * Cfg::W_BYTES, ss = sw + Cfg::SF_AT;
+          const uint32_t sx = smem_u32(smem + stage * Cfg::STAGE_BYTES);
+          const uint32_t sw = sx + Cfg::A_BYTES, ss = sx + Cfg::SF_AT;
           // this stage's scale columns: the MMAs that read them last time have
           // completed (the producer waited for their commit before refilling the stage)
           const uint32_t sf = tmem_base + Cfg::SF_COL + stage * Cfg::SF_COLS;
 #pragma unroll
           for (int i = 0; i < 3; ++i) tmem_cp_scales(sf + 4 * i, sdesc_scales(ss + i * kMxTileBytes));
 #pragma unroll
-          for (int kk = 0; kk < Cfg::KB / 32; ++kk) {
-            const uint32_t id = idesc_mx4(n, kk);
-            const uint64_t hi = sdesc_sw128(sx + kk * 32), lo = sdesc_sw128(sx + kNCH * Cfg::KB + kk * 32);
-            const uint64_t wb = sdesc_sw128(sw + kk * 32), wc = sdesc_sw128(sw + Cfg::W_BYTES + kk * 32);
-            umma_mxf8f6f4(d0, wb, hi, id, sf, sf + 8, (kb | kk) != 0);
-            umma_mxf8f6f4(d0, wb, lo, id, sf, sf + 10, 1);
-            umma_mxf8f6f4(d0 + kNCH, wc, hi, id, sf + 4, sf + 8, (kb | kk) != 0);
-            umma_mxf8f6f4(d0 + kNCH, wc, lo, id, sf + 4, sf + 10, 1);
-          }
+          for (int kk = 0; kk < Cfg::KB / 32; ++kk)
+            umma_mxf8f6f4(tmem_base, sdesc_sw128(sx + kk * 32), sdesc_sw128(sw + kk * 32), idesc_mx4(n, kk), sf, sf + 4,
+                          (kb | kk) != 0);
           umma_commit(empty + stage);
           if (++stage == S) {
             stage = 0;
@@ -376,19 +406,107 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
           }
         }
         if (!ok) break;
-        umma_commit(tfull + acc);
-        if (++acc == 2) {
-          acc = 0;
-          acc_phase ^= 1;
-        }
+        umma_commit(tfull);
+        acc_phase ^= 1;
       }
       umma_commit(drain);
       drain_wait(drain, 0);
     }
     __syncwarp();
   } else {
-    swap_epilogue<true, EPI, Cfg::EPI_WARPS>(p, s_pre, s_offs, total, tmem_base, tfull, tempty, abort_flag, tcode, warp,
-                                             lane);
+    // ------------------------------------------------ epilogue
+    // Warps of lane quarter q = warp % 4 hold tokens 16 q .. 16 q + 15 (lane pairs);
+    // the two of a quarter take half of the weight rows each.  After the planes are
+    // summed a lane has one token and 32 (SwiGLU) or 64 consecutive outputs.
+    const int q = warp & 3, eg = (warp - 2) >> 2;
+    const bool odd = lane & 1;
+    const int i = q * 32 + lane, jj = i >> 1;
+    uint32_t acc_phase = 0;
+    for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
+      const SwapTile t = decode_swap<TILE_ROWS>(p, s_pre, s_offs, tile);
+      const int64_t row = t.row0 + jj;
+      bool in = jj < t.rows - t.c0 && row < p.rows_cap;
+      int64_t dst = row;
+      float w = 1.f;
+      if (EPI == kTcSlotStore && in) {
+        dst = __ldg(p.row_dst + row);
+        w = __ldg(p.row_w + row);
+        in = dst >= 0 && in_range(dst, p.ys_rows, p.status, kSiteSlotRow);
+      }
+      if (!__all_sync(0xffffffffu, mbar_wait(tfull, acc_phase, abort_flag, p.status, tcode | 4)))
+        break;  // the warp stops as one: its TMEM loads are warp-collective
+      acc_phase ^= 1;
+      tc_fence_after();
+      const bool work = q * 16 < t.rows - t.c0 && (!HALVES || t.n0 + eg * 128 < t.N);  // (uniform in the warp)
+      uint32_t v0[32], v1[32], v2[32], v3[32];
+      if (work) {
+        const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16);
+        // SwiGLU: gate and up columns of 64 features; else 128 columns
+        tmem_ld32(tb + (HALVES ? eg * 128 : eg * 64), v0);
+        tmem_ld32(tb + (HALVES ? eg * 128 + 32 : eg * 64 + 32), v1);
+        tmem_ld32(tb + (HALVES ? eg * 128 + 64 : 128 + eg * 64), v2);
+        tmem_ld32(tb + (HALVES ? eg * 128 + 96 : 128 + eg * 64 + 32), v3);
+        tmem_wait_regs(v0);
+        tmem_wait_regs(v1);
+        tmem_wait_regs(v2);
+        tmem_wait_regs(v3);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tempty);
+      if (!work) continue;
+      if (EPI == kTcSwiGLU) {
+        mx_sum_planes(v0, v1, odd);  // gate of this lane's 32 features
+        mx_sum_planes(v2, v3, odd);  // up
+        uint32_t amax = 0;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          v0[j] = __float_as_uint(silu_f32(__uint_as_float(v0[j])) * __uint_as_float(v2[j]));
+          amax = max(amax, v0[j] & 0x7fffffffu);
+        }
+        // the activation enters the down product as two E4M3 terms, with no bf16
+        // in between: hi and lo / 16 hold it to 2^-8 of its value, as bf16 would
+        const uint32_t b = mx_split_byte(amax);
+        const float inv = mx_split_inv(b);
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const uint32_t s0 = mx_split2(__uint_as_float(v0[j]), __uint_as_float(v0[j + 1]), inv);
+          const uint32_t s1 = mx_split2(__uint_as_float(v0[j + 2]), __uint_as_float(v0[j + 3]), inv);
+          v2[j / 4] = __byte_perm(s0, s1, 0x5410);
+          v3[j / 4] = __byte_perm(s0, s1, 0x7632);
+        }
+        const int chunk = s_pre[t.g] / a.col_tiles + t.c0 / kNCH;
+        if (!in || chunk > a.max_chunk) continue;
+        const int n = t.n0 + eg * 64 + (odd ? 32 : 0);
+        uint4* h = reinterpret_cast<uint4*>(a.hl_out + 2 * row * p.ldh + n);
+        uint4* l = reinterpret_cast<uint4*>(a.hl_out + (2 * row + 1) * p.ldh + n);
+        h[0] = make_uint4(v2[0], v2[1], v2[2], v2[3]);
+        h[1] = make_uint4(v2[4], v2[5], v2[6], v2[7]);
+        l[0] = make_uint4(v3[0], v3[1], v3[2], v3[3]);
+        l[1] = make_uint4(v3[4], v3[5], v3[6], v3[7]);
+        const int ih = 2 * jj;
+        uint8_t* s = a.sf_out + ((int64_t)chunk * (p.ldh / 128) + (n >> 7)) * kMxTileBytes + (ih & 31) * 16 +
+                     (ih >> 5) * 4 + ((n & 127) >> 5);
+        s[0] = (uint8_t)b;
+        s[16] = (uint8_t)mx_lo_byte(b);
+      } else {
+        // lanes of a pair: the first and the last 64 of the warp's 128 outputs
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const uint32_t g0 = __shfl_xor_sync(0xffffffffu, odd ? v0[j] : v2[j], 1);
+          const uint32_t g1 = __shfl_xor_sync(0xffffffffu, odd ? v1[j] : v3[j], 1);
+          v0[j] = __float_as_uint(__uint_as_float(odd ? v2[j] : v0[j]) + __uint_as_float(g0));
+          v1[j] = __float_as_uint(__uint_as_float(odd ? v3[j] : v1[j]) + __uint_as_float(g1));
+        }
+        if (!in) continue;
+        const int n = t.n0 + eg * 128 + (odd ? 64 : 0);
+        bf16* o = EPI == kTcSlotStore ? p.ys + dst * p.ldy + n : p.out + row * p.ldo + n;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) reinterpret_cast<uint4*>(o)[j] = mx_bf16x8(v0 + 8 * j, w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) reinterpret_cast<uint4*>(o)[4 + j] = mx_bf16x8(v1 + 8 * j, w);
+      }
+    }
   }
 
   tc_fence_before();
