@@ -66,9 +66,8 @@ static __device__ long long g_wait_limit = kWaitLimitCycles;
 __device__ __forceinline__ long long wait_limit() { return *reinterpret_cast<volatile long long*>(&g_wait_limit); }
 
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                          unsigned* status, unsigned where) {
+                                          unsigned* status, unsigned where, long long lim) {
   if (mbar_try_wait(bar, parity)) return true;
-  const long long lim = wait_limit();
   const uint32_t mask = lim < kShortWaitLimit ? 0u : 255u;
   const long long t0 = clock64();
   for (uint32_t i = 1;; ++i) {
@@ -82,6 +81,12 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
       }
     }
   }
+}
+
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          unsigned* status, unsigned where) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, abort_flag, status, where, wait_limit());
 }
 
 // The same bounded wait, polling with the non-blocking test_wait, for a

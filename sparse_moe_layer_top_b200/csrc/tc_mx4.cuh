@@ -21,10 +21,11 @@
 // and measured 3.32 ms on the gate/up product of 2048 tokens x 10 experts at
 // d = 8192, I = 2048, E = 512.
 // A K block is 128 columns: TMA unpacks the 4-bit rows into the 8-bit containers the
-// MMA reads (16 codes per 16 bytes, 128-byte swizzle), and the scale tiles of the
-// weights (one 512-byte tile per 128 rows: their layout in memory is the tensor core's)
-// and of the tokens come as plain bulk copies.  The MMA thread moves the scale tiles
-// into TMEM (tcgen05.cp.32x128b.warpx4) ahead of the MMAs that read them.
+// MMA reads (16 codes per 16 bytes, 128-byte swizzle).  Four warps bring the scale
+// tiles of the weights (one 512-byte tile per 128 rows: its layout in memory is the
+// tensor core's) and of the tokens into TMEM from registers, ahead of the MMAs that
+// read them; copied there from shared memory by the MMA thread (tcgen05.cp), three
+// tiles cost the tensor pipe about 220 cycles per 512 cycles of MMA.
 //
 // The tile list is the one of tc_swap.cuh: the chunks of one weight tile are adjacent.
 // TMEM: one accumulator of 256 columns, then 16 scale columns per stage (tokens 4,
@@ -32,7 +33,7 @@
 // warps instead take the whole accumulator into registers (128 a thread) and hand it
 // back before they compute or store, while the loads run on.
 //
-// Warps: 0 producer; 1 TMEM owner and MMA issuer; 2..9 epilogue.
+// Warps: 0 producer; 1 TMEM owner and MMA issuer; 2..9 epilogue; 10..13 scales.
 #pragma once
 #include "mx4.cuh"
 #include "tc_swap.cuh"
@@ -45,19 +46,19 @@ struct Mx4Cfg {
   static constexpr int KB = 128;                 // columns per K block
   static constexpr int A_BYTES = 2 * kNCH * KB;  // hi and lo rows of the token chunk
   static constexpr int B_BYTES = 256 * KB;       // weight rows, unpacked
-  static constexpr int SF_AT = A_BYTES + B_BYTES;
-  static constexpr int STAGE_BYTES = (SF_AT + 3 * kMxTileBytes + 1023) / 1024 * 1024;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int SMALL = 16;               // chunks of at most this many tokens load 2 * SMALL rows of A
   // bytes the barrier counts: the unpacking loads count the packed codes they read
-  static constexpr int TX_BYTES = A_BYTES + B_BYTES / 2 + 3 * kMxTileBytes;
+  static constexpr int TX_BYTES = A_BYTES + B_BYTES / 2;
   static constexpr int TX_SMALL = TX_BYTES - A_BYTES + 2 * SMALL * KB;
   static constexpr int STAGES = 4;
   static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
   static constexpr int EPI_WARPS = 8;
-  static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+  static constexpr int SF_WARPS = 4;
+  static constexpr int THREADS = 64 + 32 * (EPI_WARPS + SF_WARPS);
   static constexpr int SF_COL = 256, SF_COLS = 16;
   static constexpr int TMEM_COLS = 512;
-  static constexpr int BAR_BYTES = (2 * STAGES + 3) * 8 + 8;
+  static constexpr int BAR_BYTES = (3 * STAGES + 3) * 8 + 8;
   static constexpr int SCHED_INTS = 2 * (512 + 2);
   static constexpr int SMEM_BYTES = 1024 + RING_BYTES + BAR_BYTES + SCHED_INTS * 4;
   static_assert(SF_COL + STAGES * SF_COLS <= TMEM_COLS, "TMEM columns");
@@ -196,19 +197,16 @@ __device__ __forceinline__ void umma_mxf8f6f4(uint32_t d_tmem, uint64_t a_desc, 
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
 }
-// A 512-byte scale tile (32 rows of 16 bytes) into 4 TMEM columns, the same 32
-// lanes repeated in every lane quarter; in order with this thread's MMAs.
-__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t sdesc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+// 32 lanes x 4 / 8 consecutive 32-bit columns into TMEM (one row per thread).
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, uint4 v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w)
+               : "memory");
 }
-// Unswizzled descriptor of a scale tile: 8-row core groups of 128 bytes.
-__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)1 << 16;
-  d |= (uint64_t)(128 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  return d;
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, uint4 v, uint4 w) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v.x),
+               "r"(v.y), "r"(v.z), "r"(v.w), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
+               : "memory");
 }
 // Instruction descriptor, .kind::mxf8f6f4: A E4M3, B E2M1, both K-major, M = 128,
 // UE8M0 scales; `id` selects the byte of each scale word (the 32-column step).
@@ -216,14 +214,6 @@ __device__ __forceinline__ uint32_t idesc_mx4(int N, int id) {
   return ((uint32_t)id << 4) | (0u << 7) | (5u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | (1u << 27) |
          ((uint32_t)id << 29);
 }
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
-          smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
-      : "memory");
-}
-
 // The accumulator's hi rows (even lanes) and lo rows (odd lanes) of 64 columns
 // (a: 0..31, b: 32..63) summed: the even lane gets columns 0..31 in a, the odd
 // lane 32..63.
@@ -270,7 +260,8 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
   uint8_t* smem = align1024(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::RING_BYTES);
   uint64_t* empty = full + S;
-  uint64_t* tfull = empty + S;
+  uint64_t* sfull = empty + S;
+  uint64_t* tfull = sfull + S;
   uint64_t* tempty = tfull + 1;
   uint64_t* drain = tempty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -280,10 +271,12 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned tcode = kStatusTimeoutBase | (kKernGemmMx4 << 8);
+  const long long lim = wait_limit();
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full + s, 1);
       mbar_init(empty + s, 1);
+      mbar_init(sfull + s, Cfg::SF_WARPS);
     }
     mbar_init(tfull, 1);
     mbar_init(tempty, Cfg::EPI_WARPS);
@@ -326,24 +319,15 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
         const SwapTile t = decode_swap<TILE_ROWS>(p, s_pre, s_offs, tile);
         const bool sh = t.g == p.E;
         const int nkb = (sh ? p.K_s : p.K_r) / Cfg::KB;
-        // scale tiles: [group][row tile][K block]; a second half past the matrix
-        // re-reads the first half's (neither it nor its codes are multiplied)
-        const int64_t rt = (int64_t)(sh ? 0 : t.g) * (t.N / 128) + t.n0 / 128;
-        const bool c_in = t.n0 + C_ROW < t.N;
         const bool small = t.rows - t.c0 <= Cfg::SMALL;
-        const uint8_t* sb = (sh ? a.sb_s : a.sb_r) + rt * nkb * kMxTileBytes;
-        const uint8_t* sc = (sh ? a.sc_s : a.sc_r) + (rt + (c_in ? C_ROW / 128 : 0)) * nkb * kMxTileBytes;
-        const uint8_t* sx =
-            a.sf + (int64_t)min(s_pre[t.g] / a.col_tiles + t.c0 / kNCH, a.max_chunk) * (a.ld / Cfg::KB) * kMxTileBytes;
         for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait(empty + stage, phase ^ 1, abort_flag, p.status, tcode | 1)) {
+          if (!mbar_wait(empty + stage, phase ^ 1, abort_flag, p.status, tcode | 1, lim)) {
             ok = false;
             break;
           }
           uint64_t* land = full + stage;
           uint8_t* base = smem + stage * Cfg::STAGE_BYTES;
           uint8_t* wb = base + Cfg::A_BYTES;
-          uint8_t* sf = base + Cfg::SF_AT;
           const int k0 = kb * Cfg::KB;
           mbar_arrive_expect_tx(land, small ? Cfg::TX_SMALL : Cfg::TX_BYTES);
           if (sh) {
@@ -354,9 +338,6 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
             tma_load_3d(wb + Cfg::B_BYTES / 2, &tmC_r, land, k0, t.n0 + C_ROW, t.g, pol_w);
           }
           tma_load_2d(base, small ? &tmXs : &tmX, land, k0, 2 * (int)t.row0, pol_x);
-          bulk_load(sf, sx + (int64_t)kb * kMxTileBytes, kMxTileBytes, land, pol_x);
-          bulk_load(sf + kMxTileBytes, sb + (int64_t)kb * kMxTileBytes, kMxTileBytes, land, pol_w);
-          bulk_load(sf + 2 * kMxTileBytes, sc + (int64_t)kb * kMxTileBytes, kMxTileBytes, land, pol_w);
           issued |= 1u << stage;
           last_par = (last_par & ~(1u << stage)) | (phase << stage);
           if (++stage == S) {
@@ -380,21 +361,18 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
         const SwapTile t = decode_swap<TILE_ROWS>(p, s_pre, s_offs, tile);
         const int n = t.n0 + C_ROW < t.N ? 256 : 128;  // weight rows that exist
         const int nkb = (t.g == p.E ? p.K_s : p.K_r) / Cfg::KB;
-        if (!mbar_wait(tempty, acc_phase ^ 1, abort_flag, p.status, tcode | 2)) break;
+        if (!mbar_wait(tempty, acc_phase ^ 1, abort_flag, p.status, tcode | 2, lim)) break;
         tc_fence_after();
         for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait(full + stage, phase, abort_flag, p.status, tcode | 3)) {
+          if (!mbar_wait(sfull + stage, phase, abort_flag, p.status, tcode | 5, lim) ||
+              !mbar_wait(full + stage, phase, abort_flag, p.status, tcode | 3, lim)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t sx = smem_u32(smem + stage * Cfg::STAGE_BYTES);
-          const uint32_t sw = sx + Cfg::A_BYTES, ss = sx + Cfg::SF_AT;
-          // this stage's scale columns: the MMAs that read them last time have
-          // completed (the producer waited for their commit before refilling the stage)
+          const uint32_t sw = sx + Cfg::A_BYTES;
           const uint32_t sf = tmem_base + Cfg::SF_COL + stage * Cfg::SF_COLS;
-#pragma unroll
-          for (int i = 0; i < 3; ++i) tmem_cp_scales(sf + 4 * i, sdesc_scales(ss + i * kMxTileBytes));
 #pragma unroll
           for (int kk = 0; kk < Cfg::KB / 32; ++kk)
             umma_mxf8f6f4(tmem_base, sdesc_sw128(sx + kk * 32), sdesc_sw128(sw + kk * 32), idesc_mx4(n, kk), sf, sf + 4,
@@ -413,6 +391,61 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
       drain_wait(drain, 0);
     }
     __syncwarp();
+  } else if (warp >= 2 + Cfg::EPI_WARPS) {
+    // ------------------------------------------------ scales into TMEM
+    // A scale tile is 32 rows of 16 bytes: row l goes to lane l of every lane quarter,
+    // its four words to four columns.  Each warp fills the quarter it can reach;
+    // the tiles of the next K blocks wait in registers.
+    constexpr int U = 4;
+    const uint32_t tq = tmem_base + Cfg::SF_COL + ((uint32_t)((warp & 3) * 32) << 16);
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+      const SwapTile t = decode_swap<TILE_ROWS>(p, s_pre, s_offs, tile);
+      const bool sh = t.g == p.E;
+      const int nkb = (sh ? p.K_s : p.K_r) / Cfg::KB;
+      // tiles: [group][row tile][K block]; a second half past the matrix takes the
+      // first half's (the MMA does not read it)
+      const int64_t rt = (int64_t)(sh ? 0 : t.g) * (t.N / 128) + t.n0 / 128;
+      const int64_t ct = rt + (t.n0 + C_ROW < t.N ? C_ROW / 128 : 0);
+      const uint4* sx = reinterpret_cast<const uint4*>(
+          a.sf + (int64_t)min(s_pre[t.g] / a.col_tiles + t.c0 / kNCH, a.max_chunk) * (a.ld / Cfg::KB) * kMxTileBytes);
+      const uint4* sb = reinterpret_cast<const uint4*>((sh ? a.sb_s : a.sb_r) + rt * nkb * kMxTileBytes);
+      const uint4* sc = reinterpret_cast<const uint4*>((sh ? a.sc_s : a.sc_r) + ct * nkb * kMxTileBytes);
+      uint4 x[U], b[U], c[U];
+      auto fetch = [&](int i, int kb) {
+        const int at = min(kb, nkb - 1) * (kMxTileBytes / 16) + lane;
+        x[i] = __ldcg(sx + at);
+        b[i] = __ldg(sb + at);
+        c[i] = __ldg(sc + at);
+      };
+#pragma unroll
+      for (int i = 0; i < U; ++i) fetch(i, i);
+      for (int kb = 0; kb < nkb && ok; kb += U) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          if (kb + i >= nkb || !ok) break;
+          // (the MMAs that read these columns last have completed)
+          if (!__all_sync(0xffffffffu, mbar_wait(empty + stage, phase ^ 1, abort_flag, p.status, tcode | 6, lim))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          tmem_st4(tq + stage * Cfg::SF_COLS, x[i]);
+          tmem_st8(tq + stage * Cfg::SF_COLS + 4, b[i], c[i]);
+          fetch(i, kb + i + U);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sfull + stage);
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+    }
   } else {
     // ------------------------------------------------ epilogue
     // Warps of lane quarter q = warp % 4 hold tokens 16 q .. 16 q + 15 (lane pairs);
@@ -433,32 +466,34 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
         w = __ldg(p.row_w + row);
         in = dst >= 0 && in_range(dst, p.ys_rows, p.status, kSiteSlotRow);
       }
-      if (!__all_sync(0xffffffffu, mbar_wait(tfull, acc_phase, abort_flag, p.status, tcode | 4)))
+      if (!__all_sync(0xffffffffu, mbar_wait(tfull, acc_phase, abort_flag, p.status, tcode | 4, lim)))
         break;  // the warp stops as one: its TMEM loads are warp-collective
       acc_phase ^= 1;
       tc_fence_after();
       const bool work = q * 16 < t.rows - t.c0 && (!HALVES || t.n0 + eg * 128 < t.N);  // (uniform in the warp)
-      uint32_t v0[32], v1[32], v2[32], v3[32];
+      // SwiGLU: v0 the gate, v2 the up sums of this lane's 32 features; else v0 and v2
+      // the lane's 64 outputs
+      uint32_t v0[32], v2[32];
       if (work) {
-        const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16);
-        // SwiGLU: gate and up columns of 64 features; else 128 columns
-        tmem_ld32(tb + (HALVES ? eg * 128 : eg * 64), v0);
-        tmem_ld32(tb + (HALVES ? eg * 128 + 32 : eg * 64 + 32), v1);
-        tmem_ld32(tb + (HALVES ? eg * 128 + 64 : 128 + eg * 64), v2);
-        tmem_ld32(tb + (HALVES ? eg * 128 + 96 : 128 + eg * 64 + 32), v3);
+        const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (HALVES ? eg * 128 : eg * 64);
+        uint32_t v1[32];
+        tmem_ld32(tb, v0);
+        tmem_ld32(tb + (HALVES ? 64 : 32), v1);
         tmem_wait_regs(v0);
         tmem_wait_regs(v1);
+        mx_sum_planes(v0, v1, odd);
+        tmem_ld32(tb + (HALVES ? 32 : 128), v2);
+        tmem_ld32(tb + (HALVES ? 96 : 160), v1);
         tmem_wait_regs(v2);
-        tmem_wait_regs(v3);
+        tmem_wait_regs(v1);
+        mx_sum_planes(v2, v1, odd);
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(tempty);
       if (!work) continue;
       if (EPI == kTcSwiGLU) {
-        mx_sum_planes(v0, v1, odd);  // gate of this lane's 32 features
-        mx_sum_planes(v2, v3, odd);  // up
-        uint32_t amax = 0;
+        uint32_t amax = 0, l8[8];
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
           v0[j] = __float_as_uint(silu_f32(__uint_as_float(v0[j])) * __uint_as_float(v2[j]));
@@ -473,7 +508,7 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
           const uint32_t s0 = mx_split2(__uint_as_float(v0[j]), __uint_as_float(v0[j + 1]), inv);
           const uint32_t s1 = mx_split2(__uint_as_float(v0[j + 2]), __uint_as_float(v0[j + 3]), inv);
           v2[j / 4] = __byte_perm(s0, s1, 0x5410);
-          v3[j / 4] = __byte_perm(s0, s1, 0x7632);
+          l8[j / 4] = __byte_perm(s0, s1, 0x7632);
         }
         const int chunk = s_pre[t.g] / a.col_tiles + t.c0 / kNCH;
         if (!in || chunk > a.max_chunk) continue;
@@ -482,29 +517,21 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
         uint4* l = reinterpret_cast<uint4*>(a.hl_out + (2 * row + 1) * p.ldh + n);
         h[0] = make_uint4(v2[0], v2[1], v2[2], v2[3]);
         h[1] = make_uint4(v2[4], v2[5], v2[6], v2[7]);
-        l[0] = make_uint4(v3[0], v3[1], v3[2], v3[3]);
-        l[1] = make_uint4(v3[4], v3[5], v3[6], v3[7]);
+        l[0] = make_uint4(l8[0], l8[1], l8[2], l8[3]);
+        l[1] = make_uint4(l8[4], l8[5], l8[6], l8[7]);
         const int ih = 2 * jj;
         uint8_t* s = a.sf_out + ((int64_t)chunk * (p.ldh / 128) + (n >> 7)) * kMxTileBytes + (ih & 31) * 16 +
                      (ih >> 5) * 4 + ((n & 127) >> 5);
         s[0] = (uint8_t)b;
         s[16] = (uint8_t)mx_lo_byte(b);
       } else {
-        // lanes of a pair: the first and the last 64 of the warp's 128 outputs
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const uint32_t g0 = __shfl_xor_sync(0xffffffffu, odd ? v0[j] : v2[j], 1);
-          const uint32_t g1 = __shfl_xor_sync(0xffffffffu, odd ? v1[j] : v3[j], 1);
-          v0[j] = __float_as_uint(__uint_as_float(odd ? v2[j] : v0[j]) + __uint_as_float(g0));
-          v1[j] = __float_as_uint(__uint_as_float(odd ? v3[j] : v1[j]) + __uint_as_float(g1));
-        }
         if (!in) continue;
         const int n = t.n0 + eg * 128 + (odd ? 64 : 0);
         bf16* o = EPI == kTcSlotStore ? p.ys + dst * p.ldy + n : p.out + row * p.ldo + n;
 #pragma unroll
         for (int j = 0; j < 4; ++j) reinterpret_cast<uint4*>(o)[j] = mx_bf16x8(v0 + 8 * j, w);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) reinterpret_cast<uint4*>(o)[4 + j] = mx_bf16x8(v1 + 8 * j, w);
+        for (int j = 0; j < 4; ++j) reinterpret_cast<uint4*>(o)[4 + j] = mx_bf16x8(v2 + 8 * j, w);
       }
     }
   }
