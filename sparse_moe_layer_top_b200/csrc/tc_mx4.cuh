@@ -26,9 +26,14 @@
 // tensor core's) and of the tokens into TMEM from registers, ahead of the MMAs that
 // read them; copied there from shared memory by the MMA thread (tcgen05.cp), three
 // tiles cost the tensor pipe about 220 cycles per 512 cycles of MMA.
+// Other ways to bring the codes, measured on the gate/up product of 2048 tokens x 10
+// experts at d = 8192, I = 2048, E = 512 (this one: 2.14 ms; its loads alone 1.64, its
+// MMAs and scales alone 1.37): 8-byte cp.async by eight warps 2.86 ms; 16-byte loads to
+// registers, stored by eight warps, 3.1 ms; weights and token rows in rings of their own,
+// 5 and 3 stages, 2.30 ms; TMA prefetches to L2 eight K blocks ahead 2.81 ms.
 //
 // The tile list is the one of tc_swap.cuh: the chunks of one weight tile are adjacent.
-// TMEM: one accumulator of 256 columns, then 16 scale columns per stage (tokens 4,
+// TMEM: one accumulator of 256 columns, then 16 groups of 16 scale columns (tokens 4,
 // weights 8).  Two accumulators and the scales do not fit 512 columns; the epilogue
 // warps instead take the whole accumulator into registers (128 a thread) and hand it
 // back before they compute or store, while the loads run on.
@@ -48,7 +53,7 @@ struct Mx4Cfg {
   static constexpr int B_BYTES = 256 * KB;       // weight rows, unpacked
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int SMALL = 16;               // chunks of at most this many tokens load 2 * SMALL rows of A
-  // bytes the barrier counts: the unpacking loads count the packed codes they read
+  // Bytes the barrier counts: the unpacking loads count the packed codes they read
   static constexpr int TX_BYTES = A_BYTES + B_BYTES / 2;
   static constexpr int TX_SMALL = TX_BYTES - A_BYTES + 2 * SMALL * KB;
   static constexpr int STAGES = 4;
@@ -56,12 +61,13 @@ struct Mx4Cfg {
   static constexpr int EPI_WARPS = 8;
   static constexpr int SF_WARPS = 4;
   static constexpr int THREADS = 64 + 32 * (EPI_WARPS + SF_WARPS);
-  static constexpr int SF_COL = 256, SF_COLS = 16;
+  // scale columns: SF_GROUPS groups of SF_KB K blocks of 16 columns (tokens 4, weights 8)
+  static constexpr int SF_COL = 256, SF_COLS = 16, SF_KB = 4, SF_GROUPS = 4;
   static constexpr int TMEM_COLS = 512;
-  static constexpr int BAR_BYTES = (3 * STAGES + 3) * 8 + 8;
+  static constexpr int BAR_BYTES = (2 * STAGES + 2 * SF_GROUPS + 3) * 8 + 8;
   static constexpr int SCHED_INTS = 2 * (512 + 2);
   static constexpr int SMEM_BYTES = 1024 + RING_BYTES + BAR_BYTES + SCHED_INTS * 4;
-  static_assert(SF_COL + STAGES * SF_COLS <= TMEM_COLS, "TMEM columns");
+  static_assert(SF_COL + SF_GROUPS * SF_KB * SF_COLS <= TMEM_COLS, "TMEM columns");
   static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0, "swizzled tiles need 1024-byte alignment");
   static_assert(SMEM_BYTES <= 232448, "shared memory");
 };
@@ -208,6 +214,16 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, uint4 v, uint4 w) {
                "r"(v.y), "r"(v.z), "r"(v.w), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
                : "memory");
 }
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
 // Instruction descriptor, .kind::mxf8f6f4: A E4M3, B E2M1, both K-major, M = 128,
 // UE8M0 scales; `id` selects the byte of each scale word (the 32-column step).
 __device__ __forceinline__ uint32_t idesc_mx4(int N, int id) {
@@ -261,7 +277,8 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::RING_BYTES);
   uint64_t* empty = full + S;
   uint64_t* sfull = empty + S;
-  uint64_t* tfull = sfull + S;
+  uint64_t* sempty = sfull + Cfg::SF_GROUPS;
+  uint64_t* tfull = sempty + Cfg::SF_GROUPS;
   uint64_t* tempty = tfull + 1;
   uint64_t* drain = tempty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -276,7 +293,10 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
     for (int s = 0; s < S; ++s) {
       mbar_init(full + s, 1);
       mbar_init(empty + s, 1);
+    }
+    for (int s = 0; s < Cfg::SF_GROUPS; ++s) {
       mbar_init(sfull + s, Cfg::SF_WARPS);
+      mbar_init(sempty + s, 1);
     }
     mbar_init(tfull, 1);
     mbar_init(tempty, Cfg::EPI_WARPS);
@@ -352,41 +372,52 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ------------------------------------------------ MMA issuer
-      int stage = 0;
-      uint32_t phase = 0, acc_phase = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-        const SwapTile t = decode_swap<TILE_ROWS>(p, s_pre, s_offs, tile);
-        const int n = t.n0 + C_ROW < t.N ? 256 : 128;  // weight rows that exist
-        const int nkb = (t.g == p.E ? p.K_s : p.K_r) / Cfg::KB;
-        if (!mbar_wait(tempty, acc_phase ^ 1, abort_flag, p.status, tcode | 2, lim)) break;
+    // ------------------------------------------------ MMA issuer: the warp waits, one lane issues
+    const bool leader = elect_one();
+    int stage = 0, sg = 0;
+    uint32_t phase = 0, sphase = 0, acc_phase = 0;
+    const uint64_t desc0 = sdesc_sw128(smem_u32(smem));
+    bool ok = true;
+    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+      const SwapTile t = decode_swap<TILE_ROWS>(p, s_pre, s_offs, tile);
+      const int n = t.n0 + C_ROW < t.N ? 256 : 128;  // weight rows that exist
+      const int nkb = (t.g == p.E ? p.K_s : p.K_r) / Cfg::KB;
+      if (!__all_sync(0xffffffffu, mbar_wait(tempty, acc_phase ^ 1, abort_flag, p.status, tcode | 2, lim))) break;
+      tc_fence_after();
+      for (int kb = 0; kb < nkb; ++kb) {
+        const int sk = kb % Cfg::SF_KB;
+        const bool got = (sk != 0 || mbar_wait(sfull + sg, sphase, abort_flag, p.status, tcode | 5, lim)) &&
+                         mbar_wait(full + stage, phase, abort_flag, p.status, tcode | 3, lim);
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
-        for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait(sfull + stage, phase, abort_flag, p.status, tcode | 5, lim) ||
-              !mbar_wait(full + stage, phase, abort_flag, p.status, tcode | 3, lim)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sx = smem_u32(smem + stage * Cfg::STAGE_BYTES);
-          const uint32_t sw = sx + Cfg::A_BYTES;
-          const uint32_t sf = tmem_base + Cfg::SF_COL + stage * Cfg::SF_COLS;
+        const uint64_t dx = desc0 + (uint32_t)(stage * (Cfg::STAGE_BYTES >> 4));
+        const uint32_t sf = tmem_base + Cfg::SF_COL + (sg * Cfg::SF_KB + sk) * Cfg::SF_COLS;
+        const bool group_end = sk == Cfg::SF_KB - 1 || kb + 1 == nkb;
+        if (leader) {
 #pragma unroll
           for (int kk = 0; kk < Cfg::KB / 32; ++kk)
-            umma_mxf8f6f4(tmem_base, sdesc_sw128(sx + kk * 32), sdesc_sw128(sw + kk * 32), idesc_mx4(n, kk), sf, sf + 4,
+            umma_mxf8f6f4(tmem_base, dx + 2 * kk, dx + (Cfg::A_BYTES >> 4) + 2 * kk, idesc_mx4(n, kk), sf, sf + 4,
                           (kb | kk) != 0);
           umma_commit(empty + stage);
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1;
-          }
+          if (group_end) umma_commit(sempty + sg);
+          if (kb + 1 == nkb) umma_commit(tfull);
         }
-        if (!ok) break;
-        umma_commit(tfull);
-        acc_phase ^= 1;
+        __syncwarp();
+        if (group_end && ++sg == Cfg::SF_GROUPS) {
+          sg = 0;
+          sphase ^= 1;
+        }
+        if (++stage == S) {
+          stage = 0;
+          phase ^= 1;
+        }
       }
+      acc_phase ^= 1;
+    }
+    if (leader) {
       umma_commit(drain);
       drain_wait(drain, 0);
     }
@@ -394,56 +425,61 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
   } else if (warp >= 2 + Cfg::EPI_WARPS) {
     // ------------------------------------------------ scales into TMEM
     // A scale tile is 32 rows of 16 bytes: row l goes to lane l of every lane quarter,
-    // its four words to four columns.  Each warp fills the quarter it can reach;
-    // the tiles of the next K blocks wait in registers.
-    constexpr int U = 4;
+    // its four words to four columns.  Each warp fills the quarter it can reach, a
+    // group of SF_KB K blocks at a time; the next group waits in registers.
+    constexpr int U = Cfg::SF_KB;
     const uint32_t tq = tmem_base + Cfg::SF_COL + ((uint32_t)((warp & 3) * 32) << 16);
-    int stage = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
-      const SwapTile t = decode_swap<TILE_ROWS>(p, s_pre, s_offs, tile);
-      const bool sh = t.g == p.E;
-      const int nkb = (sh ? p.K_s : p.K_r) / Cfg::KB;
-      // tiles: [group][row tile][K block]; a second half past the matrix takes the
-      // first half's (the MMA does not read it)
-      const int64_t rt = (int64_t)(sh ? 0 : t.g) * (t.N / 128) + t.n0 / 128;
-      const int64_t ct = rt + (t.n0 + C_ROW < t.N ? C_ROW / 128 : 0);
-      const uint4* sx = reinterpret_cast<const uint4*>(
-          a.sf + (int64_t)min(s_pre[t.g] / a.col_tiles + t.c0 / kNCH, a.max_chunk) * (a.ld / Cfg::KB) * kMxTileBytes);
-      const uint4* sb = reinterpret_cast<const uint4*>((sh ? a.sb_s : a.sb_r) + rt * nkb * kMxTileBytes);
-      const uint4* sc = reinterpret_cast<const uint4*>((sh ? a.sc_s : a.sc_r) + ct * nkb * kMxTileBytes);
-      uint4 x[U], b[U], c[U];
-      auto fetch = [&](int i, int kb) {
-        const int at = min(kb, nkb - 1) * (kMxTileBytes / 16) + lane;
+    // the next group to load
+    int ft = blockIdx.x, fk = 0, fn = 0;
+    const uint4 *sx = nullptr, *sb = nullptr, *sc = nullptr;
+    uint4 x[U], b[U], c[U];
+    auto fetch = [&]() {  // false: no group is left
+      if (ft >= total) return false;
+      if (fk == 0) {
+        const SwapTile t = decode_swap<TILE_ROWS>(p, s_pre, s_offs, ft);
+        const bool sh = t.g == p.E;
+        fn = (sh ? p.K_s : p.K_r) / Cfg::KB;
+        // tiles: [group][row tile][K block]; a second half past the matrix takes the
+        // first half's (the MMA does not read it)
+        const int64_t rt = (int64_t)(sh ? 0 : t.g) * (t.N / 128) + t.n0 / 128;
+        const int64_t ct = rt + (t.n0 + C_ROW < t.N ? C_ROW / 128 : 0);
+        sx = reinterpret_cast<const uint4*>(a.sf + (int64_t)min(s_pre[t.g] / a.col_tiles + t.c0 / kNCH, a.max_chunk) *
+                                                       (a.ld / Cfg::KB) * kMxTileBytes) + lane;
+        sb = reinterpret_cast<const uint4*>((sh ? a.sb_s : a.sb_r) + rt * fn * kMxTileBytes) + lane;
+        sc = reinterpret_cast<const uint4*>((sh ? a.sc_s : a.sc_r) + ct * fn * kMxTileBytes) + lane;
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int at = min(fk + i, fn - 1) * (kMxTileBytes / 16);  // (past the end: not read)
         x[i] = __ldcg(sx + at);
         b[i] = __ldg(sb + at);
         c[i] = __ldg(sc + at);
-      };
+      }
+      fk += U;
+      if (fk >= fn) {
+        fk = 0;
+        ft += gridDim.x;
+      }
+      return true;
+    };
+    int sg = 0;
+    uint32_t sphase = 0;
+    while (fetch()) {
+      // (the MMAs that read these columns last have completed)
+      if (!__all_sync(0xffffffffu, mbar_wait(sempty + sg, sphase ^ 1, abort_flag, p.status, tcode | 6, lim))) break;
+      tc_fence_after();
 #pragma unroll
-      for (int i = 0; i < U; ++i) fetch(i, i);
-      for (int kb = 0; kb < nkb && ok; kb += U) {
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          if (kb + i >= nkb || !ok) break;
-          // (the MMAs that read these columns last have completed)
-          if (!__all_sync(0xffffffffu, mbar_wait(empty + stage, phase ^ 1, abort_flag, p.status, tcode | 6, lim))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          tmem_st4(tq + stage * Cfg::SF_COLS, x[i]);
-          tmem_st8(tq + stage * Cfg::SF_COLS + 4, b[i], c[i]);
-          fetch(i, kb + i + U);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(sfull + stage);
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1;
-          }
-        }
+      for (int i = 0; i < U; ++i) {
+        tmem_st4(tq + (sg * U + i) * Cfg::SF_COLS, x[i]);
+        tmem_st8(tq + (sg * U + i) * Cfg::SF_COLS + 4, b[i], c[i]);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sfull + sg);
+      if (++sg == Cfg::SF_GROUPS) {
+        sg = 0;
+        sphase ^= 1;
       }
     }
   } else {
