@@ -78,6 +78,8 @@ CASES = [
     (1, 128, 1, 1, 128, 0, [1]),
     (3, 128, 2, 1, 128, 128, [0, 3]),
     (20, 256, 5, 2, 128, 256, [17, 0, 1, 16, 6]),
+    (16, 256, 5, 2, 256, 128, [17, 0, 1, 14, 0]),
+    (10, 384, 8, 8, 128, 0, [0, 80] + [0] * 6),  # more rows of one group than tokens
     (100, 384, 6, 2, 256, 128, [64, 65, 0, 7, 63, 1]),
     (150, 512, 3, 2, 640, 0, [128, 129, 43]),
     (300, 640, 4, 3, 384, 384, [700, 200, 0, 0]),
