@@ -253,10 +253,6 @@ static cudaError_t launch_router_kc(K kernel, int ctas, cudaStream_t st, const C
   return cudaLaunchKernelEx(&cfg, kernel, x, w, args, npad);
 }
 
-// Dynamic shared memory of k_decode with nb blocks of 8 token columns: two
-// buffers of every warp's partial sums.
-static int decode_smem(int nb) { return 2 * kDecodeWarps * (2 * nb * 4 * 32) * 4; }
-
 static moe_status device_info(DeviceInfo** out) {
   int dev = 0;
   CUDA_TRY(cudaGetDevice(&dev));
@@ -1865,7 +1861,7 @@ moe_status moe_ep_expand_ids(const int32_t* counts, int32_t G, int32_t E_local, 
 // ============================================================== a few tokens, one kernel
 // Workspace of moe_decode_forward.
 struct DecodeLayout {
-  size_t bar = 0, logits = 0, xs = 0, xn = 0, gate = 0, h = 0, total = 0;
+  size_t bar = 0, logits = 0, xn = 0, gate = 0, h = 0, xq = 0, xsc = 0, hq = 0, hsc = 0, total = 0;
   int splits = 1;
 };
 // Slices of d in the router's logits: enough (16 experts, slice) units to give
@@ -1886,10 +1882,17 @@ static DecodeLayout decode_layout(const moe_problem& p) {
   L.splits = decode_splits(p);
   L.bar = take(sizeof(unsigned));
   L.logits = take((size_t)L.splits * p.T * p.E * 4);
-  L.xs = take((size_t)p.T * p.d * 2);
-  L.xn = take((size_t)p.T * p.d * 2);
+  const size_t h_rows = (size_t)p.T * (p.k + 1);
+  if (p.w_dtype == MOE_BF16) {
+    L.xn = take((size_t)p.T * p.d * 2);
+  } else {
+    L.xq = take((size_t)p.T * p.d * 2);
+    L.xsc = take((size_t)(p.d / 128) * kDecodeMaxT * 4);
+    L.hq = take(h_rows * ldh_of(p) * 2);
+    L.hsc = take(h_rows * (ldh_of(p) / 128) * 4);
+  }
   L.gate = take((size_t)p.T * 4);
-  L.h = take((size_t)p.T * (p.k + 1) * ldh_of(p) * 2);
+  L.h = take(h_rows * ldh_of(p) * 2);
   L.total = o;
   return L;
 }
@@ -1902,19 +1905,30 @@ static moe_status check_decode(const moe_problem* p) {
   return MOE_OK;
 }
 
-template <int W>
-static cudaError_t launch_decode(const DecodeArgs& a, int grid, cudaStream_t st) {
+template <int W, int NB>
+static moe_status launch_decode(const DecodeArgs& a, int sms, cudaStream_t st) {
+  PROF_BEGIN("decode_route", st);
+  CUDA_TRY(launch(k_decode_route<W, NB>, sms, kDecodeThreads, 0, st, a));
+  LAUNCH_CHECK("decode_route", st);
+  pdl_reset();
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = dim3((unsigned)sms);
   cfg.blockDim = dim3((unsigned)kDecodeThreads);
-  cfg.dynamicSmemBytes = (size_t)decode_smem(a.T <= 8 ? 1 : 2);
+  cfg.dynamicSmemBytes = (size_t)decode_smem(NB);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeCooperative;  // the grid's barriers need every CTA resident
   at[0].val.cooperative = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return a.T <= 8 ? cudaLaunchKernelEx(&cfg, k_decode<W, 1>, a) : cudaLaunchKernelEx(&cfg, k_decode<W, 2>, a);
+  PROF_BEGIN("decode", st);
+  CUDA_TRY(cudaLaunchKernelEx(&cfg, k_decode<W, NB>, a));
+  LAUNCH_CHECK("decode", st);
+  return MOE_OK;
+}
+template <int W>
+static moe_status launch_decode(const DecodeArgs& a, int sms, cudaStream_t st) {
+  return a.T <= 8 ? launch_decode<W, 1>(a, sms, st) : launch_decode<W, 2>(a, sms, st);
 }
 
 extern "C" size_t moe_decode_workspace_size(const moe_problem* p) {
@@ -1957,16 +1971,6 @@ extern "C" moe_status moe_decode_forward(const moe_problem* p, const moe_block_o
   pdl_reset();
   cudaStream_t st = (cudaStream_t)stream;
   char* wsp = (char*)ws;
-  const void* xin = x;
-  float* gate = (gate_w && p->I_s > 0) ? (float*)(wsp + L.gate) : nullptr;
-  if (norm_w || gate) {
-    if ((s = launch_prologue(*p, x, norm_w, norm_w ? opt->norm_eps : 0.f, gate ? gate_w : nullptr, wsp + L.xn, gate,
-                             st)) != MOE_OK)
-      return s;
-    if (norm_w) xin = wsp + L.xn;
-  }
-  CUDA_TRY(cudaMemsetAsync(wsp + L.bar, 0, sizeof(unsigned), st));
-  pdl_reset();
   DecodeArgs a{};
   a.T = (int)p->T;
   a.d = p->d;
@@ -1974,7 +1978,9 @@ extern "C" moe_status moe_decode_forward(const moe_problem* p, const moe_block_o
   a.k = p->k;
   a.I = p->I;
   a.I_s = p->I_s;
-  a.x = (const bf16*)xin;
+  a.x = (const bf16*)x;
+  a.gamma = (const bf16*)norm_w;
+  a.eps = norm_w ? opt->norm_eps : 0.f;
   a.w_router = (const bf16*)w_router;
   a.bias = router_bias;
   a.wg = (const uint8_t*)w.wg;
@@ -1986,8 +1992,15 @@ extern "C" moe_status moe_decode_forward(const moe_problem* p, const moe_block_o
   const void* sp[6];
   scale_parts(*p, w.scales, sp);
   for (int i = 0; i < 6; ++i) a.sc[i] = (const uint8_t*)sp[i];
-  a.gate = gate;
-  a.xs = (bf16*)(wsp + L.xs);
+  if (gate_w && p->I_s > 0) {
+    a.gate_w = (const bf16*)gate_w;
+    a.gate = (float*)(wsp + L.gate);
+  }
+  a.xn = (bf16*)(wsp + L.xn);
+  a.xq = (uint8_t*)(wsp + L.xq);
+  a.xsc = (float*)(wsp + L.xsc);
+  a.hq = (uint8_t*)(wsp + L.hq);
+  a.hsc = (float*)(wsp + L.hsc);
   a.logits = (float*)(wsp + L.logits);
   a.splits = L.splits;
   a.h = (bf16*)(wsp + L.h);
@@ -1997,11 +2010,10 @@ extern "C" moe_status moe_decode_forward(const moe_problem* p, const moe_block_o
   a.y = (bf16*)y;
   a.bar = (unsigned*)(wsp + L.bar);
   a.status = dev->status;
-  PROF_BEGIN("decode", st);
-  if (p->w_dtype == MOE_BF16) CUDA_TRY(launch_decode<kDecBf16>(a, dev->sms, st));
-  else if (p->w_dtype == MOE_FP8_E4M3_B128) CUDA_TRY(launch_decode<kDecFp8>(a, dev->sms, st));
-  else CUDA_TRY(launch_decode<kDecMx4>(a, dev->sms, st));
-  LAUNCH_CHECK("decode", st);
+  if (p->w_dtype == MOE_BF16) s = launch_decode<kDecBf16>(a, dev->sms, st);
+  else if (p->w_dtype == MOE_FP8_E4M3_B128) s = launch_decode<kDecFp8>(a, dev->sms, st);
+  else s = launch_decode<kDecMx4>(a, dev->sms, st);
+  if (s != MOE_OK) return s;
   g_launches = g_launches_pending;
   return MOE_OK;
 }

@@ -1,37 +1,45 @@
-// decode.cuh -- the whole sparse MoE block for a few tokens in one kernel.
+// decode.cuh -- the whole sparse MoE block for a few tokens in two kernels.
 //
 // With T <= kDecodeMaxT tokens the block reads every active expert's weights
 // for one or two rows each: the time is the weight bytes over the HBM rate plus
-// whatever latency the launches add, so one cooperative kernel (one CTA per SM)
-// runs all of it, with two grid barriers:
-//   1. router logits, split over (16 experts) x (slices of d): fp32 partials;
-//   -- barrier --
-//   2. every CTA adds the partials in slice order and selects each token's top k
+// whatever latency the launches and barriers add.
+//   k_decode_route: the RMSNorm, the shared expert's gate, the router's logits
+//     (split over 16 experts x slices of d, fp32 partials) and, for E4M3 and mx4
+//     weights, x as their products take it (below);
+//   k_decode, cooperative, one CTA per SM:
+//   1. every CTA adds the partials in slice order and selects each token's top k
 //      (one warp per token; the same code and inputs, so the same result in every
 //      CTA), and lists the active experts;
-//   3. gate/up: h[t, slot, f] = w * SiLU(W_g[f] x_t) * (W_u[f] x_t) in bf16, units of 16
+//   2. gate/up: h[t, slot, f] = w * SiLU(W_g[f] x_t) * (W_u[f] x_t) in bf16, units of 16
 //      features of one expert.  The routing weight w is applied here, so that
-//   -- barrier --
-//   4. the down projection is ONE sum per output: y[t, n] = sum over the active
+//   -- grid barrier (E4M3, mx4: h is prepared like x, and another barrier) --
+//   3. the down projection is ONE sum per output: y[t, n] = sum over the active
 //      experts and their features of W_d[n, f] h[t, slot, f], units of 16 outputs
 //      over all experts; fp32 throughout, rounded once, no atomics: reproducible.
 //
-// The products run on mma.sync.m16n8k16 (bf16, fp32 accumulate) with the 16
-// weight rows as M and the tokens (8 columns, two blocks of them above 8 tokens)
-// as N.  Weight fragments are loaded straight from global memory in 16-byte
-// pieces, one row per lane group and four adjacent pieces per row: the K order
-// inside a fragment is free as long as both operands share it, so lane c simply
-// takes the c-th 16 bytes of the row's chunk.  At these sizes the kernel is bound by the bytes it
-// keeps in flight, not by the tensor core (one m16n8k16 per 512 weight bytes), and
-// registers as the landing place need no shared-memory round trip.
-// E4M3 and mx4 codes become bf16 in registers by moving the code's exponent and
-// mantissa bits under bf16's (exact) and one bf16 multiply by a power of two;
-// E4M3 block scales multiply the fp32 sums of each 128-column block.
+// The products run on mma.sync with the 16 weight rows as M and the tokens (8
+// columns, two blocks of them above 8 tokens) as N; at these sizes the tensor core
+// is idle most of the time and what counts is the bytes in flight and the
+// instructions per weight byte.
+//   bytes: every warp streams its pieces (16 rows x 64 bytes) through a ring of its own
+//     in shared memory by cp.async, kDecStages stages of two pieces deep, over unit
+//     boundaries and, for the down projection's first pieces, from before the barrier:
+//     no block-wide step waits for memory.
+//   instructions: bf16 weights go to m16n8k16 as they are, E4M3 codes to m16n8k32 as
+//     they are, mx4 codes are converted to f16 two at a time.  For the last two the
+//     tokens' values are scaled by a power of two per 128 columns: for mx4 to f16, the
+//     largest in [2^14, 2^15), which holds a bf16 exactly down to 2^-31 of it; for E4M3
+//     to the sum of two E4M3 terms, x = s (hi + lo), the largest in (224, 448]: hi has
+//     four significant bits, lo the rest, exact down to 2^-9 of that largest and off by
+//     at most 2^-17 of it below.
+//     8 tokens at d = 8192, I = 2048, E = 512, k = 10, mx4: with the codes converted to
+//     bf16 by bit moves (20 operations per 8 codes at half rate) and fragments loaded
+//     straight into registers 852 us.
 // Tokens an expert was not chosen for are zero columns of its product.
 //
-// A team of kw warps shares a unit, splitting its K chunks, and adds its parts
+// A team of kw warps shares a unit, splitting its K pieces, and adds its parts
 // through shared memory in warp order; kw is picked per phase from the unit and
-// chunk counts (team_warps).
+// piece counts (team_warps).
 #pragma once
 #include "common.cuh"
 #include "mx4.cuh"
@@ -43,84 +51,59 @@ constexpr int kDecodeMaxT = 16;
 constexpr int kDecodeThreads = 512;
 constexpr int kDecodeWarps = kDecodeThreads / 32;
 constexpr int kDecodeMaxSplit = 16;  // slices of d in the router's partial logits
+constexpr int kDecStages = 3;        // ring stages of a warp
+constexpr int kDecPiece = 16 * 64;   // bytes of a piece
+constexpr int kDecScales = 64;       // bytes of its scales
+constexpr int kDecStage = 2 * (kDecPiece + kDecScales);
 enum : unsigned { kKernDecode = 4 };
+
+// Dynamic shared memory with nb blocks of 8 token columns: the rings, and a
+// buffer of every warp's partial sums.
+constexpr int decode_smem(int nb) { return kDecodeWarps * (kDecStages * kDecStage + 2 * nb * 4 * 32 * 4); }
 
 struct DecodeArgs {
   int T, d, E, k, I, I_s;
-  const bf16* x;        // [T, d] the block's (normalised) input
+  const bf16* x;        // [T, d] the block's input
+  const bf16* gamma;    // [d] RMSNorm weight, or NULL
+  float eps;
+  const bf16* gate_w;   // [d] shared expert's gate, or NULL
   const bf16* w_router; // [E, d]
   const float* bias;    // [E] or NULL
   const uint8_t *wg, *wu, *wd, *sg, *su, *sd;
   const uint8_t* sc[6]; // scale parts: gate, up, down, shared gate, up, down
-  const float* gate;    // [T] weight of the shared expert, or NULL (1)
-  bf16* xs;             // [T, d] x in the weight type's K order (E4M3, mx4)
+  float* gate;          // [T] weight of the shared expert, or NULL (1)
+  bf16* xn;             // [T, d] the normalised input (bf16 weights with a norm)
+  uint8_t* xq;          // [T][d / 32][64] x, scaled: f16 (mx4) or E4M3 terms (dec_term_place)
+  float* xsc;           // [d / 128][kDecodeMaxT] its scales
   float* logits;        // [splits][T][E] partial logits
   int splits;
   bf16* h;              // [T, k + 1, ldh]
+  uint8_t* hq;          // [T * (k + 1)][ldh / 32][64] h, scaled likewise
+  float* hsc;           // [T * (k + 1)][ldh / 128] its scales
   int ldh;
   int32_t* ids;         // [T, k] or NULL
   float* tw;            // [T, k] or NULL
   bf16* y;              // [T, d]
-  unsigned* bar;        // grid-barrier counter, zero at launch
+  unsigned* bar;        // grid-barrier counter, zeroed by k_decode_route
   unsigned* status;
 };
 
 // -------------------------------------------------------------- weight types
-// LD: 16-byte pieces a lane loads per row and chunk; CH: K columns of a chunk;
-// MM: mma steps per chunk; BW: 32-bit words of token data a lane holds per chunk.
+// PC: K columns of a piece (64 bytes of a row); BV: 16-byte vectors of token data
+// a lane holds per piece.
 enum { kDecBf16 = 0, kDecFp8 = 1, kDecMx4 = 2 };
 template <int W>
-struct DecW;
-template <>
-struct DecW<kDecBf16> {
-  static constexpr int CH = 32, LD = 1, MM = 2, BW = 4;
-  static __device__ __forceinline__ int64_t bytes(int64_t n) { return 2 * n; }
-};
-template <>
-struct DecW<kDecFp8> {
-  static constexpr int CH = 128, LD = 2, MM = 8, BW = 16;
-  static __device__ __forceinline__ int64_t bytes(int64_t n) { return n; }
-};
-template <>
-struct DecW<kDecMx4> {
-  static constexpr int CH = 128, LD = 1, MM = 8, BW = 16;
-  static __device__ __forceinline__ int64_t bytes(int64_t n) { return n >> 1; }
+struct DecW {
+  static constexpr int PC = W == kDecBf16 ? 32 : W == kDecFp8 ? 64 : 128;
+  static constexpr int BV = W == kDecBf16 ? 1 : W == kDecFp8 ? 2 : 4;
+  static constexpr bool SCALED = W != kDecBf16;  // token values under a scale per 128 columns
+  static __device__ __forceinline__ int64_t bytes(int64_t n) { return W == kDecBf16 ? 2 * n : W == kDecFp8 ? n : n >> 1; }
 };
 
-// Where element e of a row goes in the K order the converters below produce:
-// E4M3 pairs codes (0, 2) and (1, 3) of a word, mx4 codes (i, i + 4).
-template <int W>
-__device__ __forceinline__ int dec_place(int e) {
-  if (W == kDecFp8) return (e & ~3) | ((e & 1) << 1) | ((e >> 1) & 1);
-  if (W == kDecMx4) return (e & ~7) | ((e & 3) << 1) | ((e >> 2) & 1);
-  return e;
-}
-
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-// Four E4M3 codes -> bf16 pairs (codes 0, 2) and (codes 1, 3).  The seven low
-// bits of a code, four places up in a bf16, read as code * 2^-120 (also for
-// subnormal codes), so one multiply by 2^120 gives the value.
-__device__ __forceinline__ void dec_e4m3x4(uint32_t q, uint32_t& p02, uint32_t& p13) {
-  const uint32_t l = q << 8;
-  const uint32_t a = (l & 0x80008000u) | ((l >> 4) & 0x07f007f0u);
-  const uint32_t b = (q & 0x80008000u) | ((q >> 4) & 0x07f007f0u);
-  p02 = mul_bf16x2(a, 0x7b807b80u);
-  p13 = mul_bf16x2(b, 0x7b807b80u);
-}
-// Eight mx4 codes -> four bf16 pairs (i, i + 4), scaled: exponent and mantissa
-// bits six places up read as code * 2^-126; m1 (and m2) make up 2^126 * scale.
-__device__ __forceinline__ void dec_mx4x8(uint32_t q, uint32_t m1, uint32_t (&p)[4]) {
-  p[0] = ((q << 12) & 0x80008000u) | ((q << 6) & 0x01c001c0u);
-  p[1] = ((q << 8) & 0x80008000u) | ((q << 2) & 0x01c001c0u);
-  p[2] = ((q << 4) & 0x80008000u) | ((q >> 2) & 0x01c001c0u);
-  p[3] = (q & 0x80008000u) | ((q >> 6) & 0x01c001c0u);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) p[i] = mul_bf16x2(p[i], m1);
-}
+// Place of element e (0..31) of a 32-column block in its 64 bytes of E4M3 terms: lane
+// c of a lane group takes 16 bytes, the hi terms of columns 4c.. and 16 + 4c.., then
+// their lo terms.  (hi; the lo term is 8 bytes further)
+__device__ __forceinline__ int dec_term_place(int e) { return ((e & 15) >> 2) * 16 + (e >> 4) * 4 + (e & 3); }
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
@@ -129,179 +112,229 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-
-// Weight bytes pass through once: no L1 allocation.
-__device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Four 8x8 tiles of 16-bit elements, one row address a lane: word c of row g of each.
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
   return v;
 }
-
-// One 16-row weight operand of a unit: this lane's rows are g and g + 8.
-template <int W>
-struct DecRows {
-  const uint8_t* p;   // row g, this lane's piece of chunk 0
-  int64_t step8;      // bytes from row g to row g + 8
-  const uint8_t* sc;  // E4M3: fp32 scales of the row block; mx4: scale byte of row g, this lane's block, chunk 0
-  bool ok0, ok8;      // rows inside the matrix
-};
-template <int W>
-struct DecFrag {
-  uint4 lo[DecW<W>::LD], hi[DecW<W>::LD];
-  uint32_t s0, s8;  // E4M3: fp32 scale bits (s0); mx4: scale bytes of the two rows
-};
-
-// rows n0 .. n0 + 15 of matrix `m` [N, K] of the stack at w (scales sc)
-template <int W>
-__device__ __forceinline__ DecRows<W> dec_rows(const uint8_t* w, const uint8_t* sc, int64_t m, int N, int K, int n0,
-                                               int g, int c) {
-  DecRows<W> r;
-  const int64_t row = m * N + n0 + g;
-  r.p = w + DecW<W>::bytes(row * K) + c * 16;
-  r.step8 = DecW<W>::bytes((int64_t)8 * K);
-  r.ok0 = n0 + g < N;
-  r.ok8 = n0 + g + 8 < N;
-  if (W == kDecFp8)
-    r.sc = sc + 4 * ((m * (N >> 7) + (n0 >> 7)) * (int64_t)(K >> 7));
-  else if (W == kDecMx4)
-    r.sc = sc + (m * (N >> 7)) * (int64_t)(K >> 7) * kMxTileBytes + mx4_scale_at(n0 + g, c, K >> 7);
-  else
-    r.sc = nullptr;
-  return r;
+__device__ __forceinline__ void lds128(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+// 16 bytes global -> shared past L1 (zeros where ok is false); 4 bytes.
+__device__ __forceinline__ void dec_copy16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16u : 0u) : "memory");
+}
+__device__ __forceinline__ void dec_copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void dec_copy4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// Chunk kc of the operand (kpiece: columns of this lane's piece that exist).
-template <int W>
-__device__ __forceinline__ void dec_load(DecFrag<W>& f, const DecRows<W>& r, int kc, bool kok) {
-  const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-  for (int i = 0; i < DecW<W>::LD; ++i) {
-    const uint8_t* q = r.p + (int64_t)kc * (64 * DecW<W>::LD) + i * 64;
-    f.lo[i] = kok && r.ok0 ? ld_stream(q) : z;
-    f.hi[i] = kok && r.ok8 ? ld_stream(q + r.step8) : z;
-  }
-  f.s0 = f.s8 = 0;
-  if (W == kDecFp8) f.s0 = kok ? __ldg(reinterpret_cast<const uint32_t*>(r.sc) + kc) : 0u;
-  if (W == kDecMx4 && kok) {
-    f.s0 = __ldg(r.sc + (int64_t)kc * kMxTileBytes);
-    f.s8 = __ldg(r.sc + (int64_t)kc * kMxTileBytes + 8 * 16);
-  }
-}
+// -------------------------------------------------------------- pieces
+// A piece's rows are 64 bytes apart in shared memory, its 16-byte units swizzled
+// so that a fragment load meets every bank once.
+__device__ __forceinline__ uint32_t dec_unit(int row, int u) { return row * 64 + ((u ^ ((row >> 1) & 3)) << 4); }
 
-// acc[nb] += A * B over one chunk.  bw[nb]: the lane's token words.
-template <int W, int NB>
-__device__ __forceinline__ void dec_mma(float (&acc)[NB][4], const DecFrag<W>& f, const uint32_t (&bw)[NB][DecW<W>::BW],
-                                        unsigned nbmask) {
+// Bytes from the start of a matrix of K columns to row r, lane unit c, of piece 0.
+template <int W>
+__device__ __forceinline__ int64_t dec_row_at(int r, int K, int c) {
+  return DecW<W>::bytes((int64_t)r * K) + c * 16;
+}
+// Copy 16 rows x 64 bytes at q (row g, this lane's unit) to slot `at`; step8: bytes of
+// eight rows.  Only bf16 matrices end inside a piece: ok0, ok8 (rows g, g + 8 and the
+// lane's columns exist).
+template <int W>
+__device__ __forceinline__ void dec_issue(uint32_t at, const uint8_t* q, int64_t step8, bool ok0, bool ok8) {
   if (W == kDecBf16) {
-    const uint32_t l[4] = {f.lo[0].x, f.lo[0].y, f.lo[0].z, f.lo[0].w};
-    const uint32_t h[4] = {f.hi[0].x, f.hi[0].y, f.hi[0].z, f.hi[0].w};
+    dec_copy16(at, q, ok0);
+    dec_copy16(at + 512, ok8 ? q + step8 : q, ok8);
+  } else {
+    dec_copy16(at, q);
+    dec_copy16(at + 512, q + step8);
+  }
+}
+
+// A piece's fragment: rows g (lo) and g + 8 (hi).  bf16: the lane's own 16 bytes (the
+// K order inside a fragment is free as long as both operands share it); else word c of
+// each 16-byte unit.  s0, s8: mx4, the scale bytes of the rows; E4M3, s0 the scale.
+struct DecFrag {
+  uint32_t lo[4], hi[4], s0, s8;
+};
+template <int W>
+__device__ __forceinline__ void dec_read(DecFrag& f, uint32_t at, uint32_t sc_at, int lane) {
+  if (W == kDecBf16) {
+    const uint32_t d = at + dec_unit(lane >> 2, lane & 3);
+    lds128(f.lo, d);
+    lds128(f.hi, d + 512);
+    f.s0 = f.s8 = 0;
+  } else {
+    const uint32_t d = at + dec_unit(lane & 7, lane >> 3);
+    ldmatrix4(f.lo, d);
+    ldmatrix4(f.hi, d + 512);
+    f.s0 = lds32(sc_at + (W == kDecMx4 ? (lane >> 2) * 4 : 0));
+    f.s8 = W == kDecMx4 ? lds32(sc_at + (lane >> 2) * 4 + 32) : 0u;
+  }
+}
+
+// Eight mx4 codes -> four f16 pairs of consecutive values.
+__device__ __forceinline__ void mx4_to_f16(uint32_t q, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(q));
+}
+// Some byte of w is 0 or 255.
+__device__ __forceinline__ bool has_edge_byte(uint32_t w) {
+  return (((w - 0x01010101u) & ~w) | ((~w - 0x01010101u) & w)) & 0x80808080u;
+}
+
+// acc[nb] += A * B over one piece.  bw[nb]: the lane's token data; xs[nb]: scales of
+// its two token columns.  A column block whose mask bit is clear is skipped.
+template <int W, int NB>
+__device__ __forceinline__ void dec_mma(float (&acc)[NB][4], const DecFrag& f, const uint4 (&bw)[NB][DecW<W>::BV],
+                                        const float2 (&xs)[NB], unsigned nbmask) {
+  if (W == kDecBf16) {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+      if (nbmask >> nb & 1u) {
+        mma_bf16(acc[nb], f.lo[0], f.hi[0], f.lo[1], f.hi[1], bw[nb][0].x, bw[nb][0].y);
+        mma_bf16(acc[nb], f.lo[2], f.hi[2], f.lo[3], f.hi[3], bw[nb][0].z, bw[nb][0].w);
+      }
+  } else if (W == kDecFp8) {
+    const float sc = __uint_as_float(f.s0);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+      if (nbmask >> nb & 1u) {
+        float p[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 b = bw[nb][i % DecW<W>::BV];
+          mma_e4m3(p, f.lo[2 * i], f.hi[2 * i], f.lo[2 * i + 1], f.hi[2 * i + 1], b.x, b.y);
+          mma_e4m3(p, f.lo[2 * i], f.hi[2 * i], f.lo[2 * i + 1], f.hi[2 * i + 1], b.z, b.w);
+        }
+        const float s0 = sc * xs[nb].x, s1 = sc * xs[nb].y;
+        acc[nb][0] = fmaf(s0, p[0], acc[nb][0]);
+        acc[nb][1] = fmaf(s1, p[1], acc[nb][1]);
+        acc[nb][2] = fmaf(s0, p[2], acc[nb][2]);
+        acc[nb][3] = fmaf(s1, p[3], acc[nb][3]);
+      }
+  } else {
+    float s0[4], s8[4];
+    if (__any_sync(0xffffffffu, has_edge_byte(f.s0) || has_edge_byte(f.s8))) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        s0[b] = __uint_as_float(mx4_scale_bits(f.s0 >> (8 * b) & 255u));
+        s8[b] = __uint_as_float(mx4_scale_bits(f.s8 >> (8 * b) & 255u));
+      }
+    } else {
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {  // the byte at the top, under the sign
+        s0[b] = __uint_as_float(__byte_perm(f.s0, 0, b << 12 | 0x444) >> 1);
+        s8[b] = __uint_as_float(__byte_perm(f.s8, 0, b << 12 | 0x444) >> 1);
+      }
+    }
+    float sum[NB][4];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[nb][i] = 0.f;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      uint32_t l[4], h[4];
+      mx4_to_f16(f.lo[b], l);
+      mx4_to_f16(f.hi[b], h);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+        if (nbmask >> nb & 1u) {
+          const uint4 t = bw[nb][b % DecW<W>::BV];
+          float p[4] = {0.f, 0.f, 0.f, 0.f};
+          mma_f16(p, l[0], h[0], l[1], h[1], t.x, t.y);
+          mma_f16(p, l[2], h[2], l[3], h[3], t.z, t.w);
+          sum[nb][0] = fmaf(s0[b], p[0], sum[nb][0]);
+          sum[nb][1] = fmaf(s0[b], p[1], sum[nb][1]);
+          sum[nb][2] = fmaf(s8[b], p[2], sum[nb][2]);
+          sum[nb][3] = fmaf(s8[b], p[3], sum[nb][3]);
+        }
+    }
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
       if (nbmask >> nb & 1u)
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-          mma_bf16(acc[nb], l[2 * s], h[2 * s], l[2 * s + 1], h[2 * s + 1], bw[nb][2 * s], bw[nb][2 * s + 1]);
-  } else if (W == kDecFp8) {
-    float part[NB][4];
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) part[nb][i] = 0.f;
-    uint32_t nan_l = 0, nan_h = 0;  // bit 7 of a byte: a NaN code (0x7f, 0xff) was there
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t l[4] = {f.lo[i % DecW<W>::LD].x, f.lo[i % DecW<W>::LD].y, f.lo[i % DecW<W>::LD].z,
-                             f.lo[i % DecW<W>::LD].w};
-      const uint32_t h[4] = {f.hi[i % DecW<W>::LD].x, f.hi[i % DecW<W>::LD].y, f.hi[i % DecW<W>::LD].z,
-                             f.hi[i % DecW<W>::LD].w};
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        uint32_t a0, a2, a1, a3;
-        dec_e4m3x4(l[s], a0, a2);
-        dec_e4m3x4(h[s], a1, a3);
-        nan_l |= (l[s] & 0x7f7f7f7fu) + 0x01010101u;
-        nan_h |= (h[s] & 0x7f7f7f7fu) + 0x01010101u;
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-          if (nbmask >> nb & 1u)
-            mma_bf16(part[nb], a0, a1, a2, a3, bw[nb][(i * 8 + 2 * s) % DecW<W>::BW],
-                     bw[nb][(i * 8 + 2 * s + 1) % DecW<W>::BW]);
-      }
-    }
-    const float sc = __uint_as_float(f.s0);
-    const unsigned bad = ((nan_l & 0x80808080u) ? 1u : 0u) | ((nan_h & 0x80808080u) ? 2u : 0u);
-    if (__any_sync(0xffffffffu, bad)) {  // the bit move reads them as 480: a row holding one is NaN
-      unsigned row = bad | __shfl_xor_sync(0xffffffffu, bad, 1);
-      row |= __shfl_xor_sync(0xffffffffu, row, 2);
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (row >> (i >> 1) & 1u) part[nb][i] = __int_as_float(0x7fffffff);
-    }
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[nb][i] = fmaf(sc, part[nb][i], acc[nb][i]);
-  } else {
-    // 2^126 * scale as one bf16 factor while it is one (scale <= 2), else as two
-    const bool big = f.s0 > 128u || f.s8 > 128u;
-    uint32_t m0 = (min(f.s0, 128u) + 126u) << 7, m8 = (min(f.s8, 128u) + 126u) << 7;
-    m0 |= m0 << 16;
-    m8 |= m8 << 16;
-    const bool any_big = __any_sync(0xffffffffu, big);
-    const uint32_t l[4] = {f.lo[0].x, f.lo[0].y, f.lo[0].z, f.lo[0].w};
-    const uint32_t h[4] = {f.hi[0].x, f.hi[0].y, f.hi[0].z, f.hi[0].w};
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      uint32_t a[4], b[4];
-      dec_mx4x8(l[w], m0, a);
-      dec_mx4x8(h[w], m8, b);
-      if (any_big) {
-        uint32_t e0 = f.s0 == 255u ? 0x7fffu : (max(f.s0, 128u) - 1u) << 7;
-        uint32_t e8 = f.s8 == 255u ? 0x7fffu : (max(f.s8, 128u) - 1u) << 7;
-        e0 |= e0 << 16;
-        e8 |= e8 << 16;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          a[i] = mul_bf16x2(a[i], e0);
-          b[i] = mul_bf16x2(b[i], e8);
-        }
-      }
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-          if (nbmask >> nb & 1u)
-            mma_bf16(acc[nb], a[2 * s], b[2 * s], a[2 * s + 1], b[2 * s + 1],
-                     bw[nb][(4 * w + 2 * s) % DecW<W>::BW], bw[nb][(4 * w + 2 * s + 1) % DecW<W>::BW]);
-    }
+        for (int i = 0; i < 4; ++i) acc[nb][i] = fmaf(i & 1 ? xs[nb].y : xs[nb].x, sum[nb][i], acc[nb][i]);
   }
 }
 
-// Token words of one chunk for the lane's token (p: its row at this lane's
-// piece of chunk 0, NULL: a zero column).  E4M3 pieces are 32 bf16 apart twice.
+// Token data of piece kc for the lane's token column (p: its row, NULL: zeros).
 template <int W>
-__device__ __forceinline__ void dec_tok(uint32_t (&bw)[DecW<W>::BW], const bf16* p, int kc, bool kok) {
-  const uint4* q = reinterpret_cast<const uint4*>(p + (int64_t)kc * DecW<W>::CH);
+__device__ __forceinline__ void dec_tok(uint4 (&bw)[DecW<W>::BV], const uint8_t* p, int kc, int K, int c) {
+  // bf16: 8 columns a lane; terms: 16 bytes a lane and 32-column block
+  const bool ok = p && (W != kDecBf16 || kc * 32 + c * 8 < K);
 #pragma unroll
-  for (int i = 0; i < DecW<W>::BW / 4; ++i) {
-    // bf16: 8 columns a lane; E4M3: 16 at c * 16 and 16 at 64 + c * 16; mx4: 32 at c * 32
-    const int at = W == kDecFp8 ? (i & 1) + (i >> 1) * 8 : i;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (p && kok) v = *(q + at);
-    bw[4 * i] = v.x;
-    bw[4 * i + 1] = v.y;
-    bw[4 * i + 2] = v.z;
-    bw[4 * i + 3] = v.w;
+  for (int i = 0; i < DecW<W>::BV; ++i) {
+    bw[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (ok) bw[i] = *reinterpret_cast<const uint4*>(p + ((int64_t)kc * DecW<W>::BV + i) * 64 + c * 16);
   }
 }
-// columns of a lane's first piece: the offset of its token data in a chunk
+
+// -------------------------------------------------------------- scaled tokens
+// Four consecutive values a lane, 128 columns a warp: scaled to q (the 128 columns'
+// 256 bytes), the scale to *sc.  A block holding an infinity or a NaN becomes NaN.
 template <int W>
-__device__ __forceinline__ int dec_tok_off(int c) {
-  return c * (W == kDecMx4 ? 32 : W == kDecFp8 ? 16 : 8);
+__device__ __forceinline__ void dec_split(const float (&v)[4], uint8_t* q, float* sc, int lane) {
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);
+  amax = __reduce_max_sync(0xffffffffu, amax);
+  const float nan = __uint_as_float(0x7fffffffu);
+  if (W == kDecMx4) {
+    const uint32_t e = max(amax >> 23, 15u);
+    const float inv = e == 255u ? nan : __uint_as_float((268u - e) << 23);  // 2^(14 - exponent)
+    const __half2 a = __floats2half2_rn(v[0] * inv, v[1] * inv), b = __floats2half2_rn(v[2] * inv, v[3] * inv);
+    *reinterpret_cast<uint2*>(q + lane * 8) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    if (lane == 0) *sc = e == 255u ? nan : __uint_as_float((e - 14u) << 23);
+  } else {
+    const uint32_t b = mx_split_byte(amax);
+    const float inv = mx_split_inv(b);
+    uint32_t h[2], l[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float a0 = v[2 * i] * inv, a1 = v[2 * i + 1] * inv;
+      h[i] = e4m3x2(a0, a1);
+      const float2 w = e4m3x2_value(h[i]);
+      l[i] = e4m3x2(a0 - w.x, a1 - w.y);
+    }
+    uint8_t* o = q + (lane >> 3) * 64 + dec_term_place((lane & 7) * 4);
+    *reinterpret_cast<uint32_t*>(o) = h[0] | h[1] << 16;
+    *reinterpret_cast<uint32_t*>(o + 8) = l[0] | l[1] << 16;
+    if (lane == 0) *sc = b == 255u ? nan : __uint_as_float(b << 23);
+  }
 }
 
 // All CTAs of the cooperative grid have reached round `n` (1, 2, ..) of the
@@ -361,52 +394,42 @@ struct DecShared {
   int32_t flag[512];
   int32_t rank[512];
   int32_t wsum[kDecodeWarps];
+  // down projection: the active experts' (then the shared expert's) matrices and scales
+  const uint8_t* wd[kDecodeMaxT * kMaxK + 1];
+  const uint8_t* sc[kDecodeMaxT * kMaxK + 1];
   int n_act, kw1, kw2, ok;
 };
 
-// Top k of one token's logits by one warp: k rounds of (largest key, lowest
+// Top k of one token's logits (l) by one warp: k rounds of (largest key, lowest
 // expert holding it).  Keys order as the logits; NaN sorts below every number.
 template <int NPL>
-__device__ __forceinline__ void dec_topk(const DecodeArgs& a, int t, DecShared& s) {
+__device__ __forceinline__ void dec_topk(const float* logits, int E, int k, int t, DecShared& s) {
   const int lane = threadIdx.x & 31;
   float l[NPL];
   uint32_t key[NPL];
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
     const int e = lane + 32 * i;
-    l[i] = e < a.E && a.bias ? __ldg(a.bias + e) : 0.f;
-  }
-  for (int p = 0; p < a.splits; ++p) {
-    const float* row = a.logits + ((int64_t)p * a.T + t) * a.E;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i)
-      if (lane + 32 * i < a.E) l[i] += __ldcg(row + lane + 32 * i);
-  }
-#pragma unroll
-  for (int i = 0; i < NPL; ++i) {
+    l[i] = e < E ? logits[e] : 0.f;
     const uint32_t u = __float_as_uint(l[i]);
     // order-preserving map, kept above 0 (taken or absent) and 1 (NaN)
     uint32_t q = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
     if (l[i] != l[i]) q = 1u;
-    key[i] = lane + 32 * i < a.E ? q : 0u;
+    key[i] = e < E ? q : 0u;
   }
   float v0 = 0.f, den = 0.f, my_v = 0.f;
   int my_e = 0;
-  for (int j = 0; j < a.k; ++j) {
+  for (int j = 0; j < k; ++j) {
     uint32_t best = 0;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) best = max(best, key[i]);
     const uint32_t top = __reduce_max_sync(0xffffffffu, best);
     unsigned cand = 0xffffffffu;
-    float cv = 0.f;
 #pragma unroll
     for (int i = NPL - 1; i >= 0; --i)
-      if (key[i] == top && lane + 32 * i < a.E) {
-        cand = lane + 32 * i;
-        cv = l[i];
-      }
+      if (key[i] == top && lane + 32 * i < E) cand = lane + 32 * i;
     const unsigned e = __reduce_min_sync(0xffffffffu, cand);
-    const float v = __shfl_sync(0xffffffffu, cv, e & 31);
+    const float v = logits[e];
 #pragma unroll
     for (int i = 0; i < NPL; ++i)
       if (e == (unsigned)(lane + 32 * i)) key[i] = 0u;
@@ -417,94 +440,184 @@ __device__ __forceinline__ void dec_topk(const DecodeArgs& a, int t, DecShared& 
       my_e = (int)e;
     }
   }
-  if (lane < a.k) {
+  if (lane < k) {
     s.ids[t][lane] = my_e;
     s.w[t][lane] = expf(my_v - v0) / den;
   }
 }
 
-// -------------------------------------------------------------- the kernel
+// -------------------------------------------------------------- norm, gate, logits
+// Eight values of x, normalised: v * r * (1 + gamma), rounded to bf16.
+__device__ __forceinline__ uint4 dec_norm8(uint4 x, uint4 gamma, float r) {
+  const uint32_t a[4] = {x.x, x.y, x.z, x.w}, g[4] = {gamma.x, gamma.y, gamma.z, gamma.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o[i] = pack_bf16x2(__uint_as_float(a[i] << 16) * r * (1.0f + __uint_as_float(g[i] << 16)),
+                       __uint_as_float(a[i] & 0xffff0000u) * r * (1.0f + __uint_as_float(g[i] & 0xffff0000u)));
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+__device__ __forceinline__ float dec_warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+template <int W, int NB>
+__global__ void __launch_bounds__(kDecodeThreads, 1) k_decode_route(const DecodeArgs a) {
+  pdl_begin();  // after the previous kernel in the stream (programmatic launch)
+  __shared__ float s_r[kDecodeMaxT];
+  __shared__ float red[kDecodeWarps][NB * 128];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, c = lane & 3;
+  if (blockIdx.x == 0 && tid == 0) *a.bar = 0;
+  const uint4* gam = reinterpret_cast<const uint4*>(a.gamma);
+  if (a.gamma) {  // 1 / rms of every token, in every CTA alike
+    if (warp < a.T) {
+      const uint4* row = reinterpret_cast<const uint4*>(a.x + (int64_t)warp * a.d);
+      float ss = 0.f;
+#pragma unroll 8
+      for (int j = lane; j < a.d / 8; j += 32) {
+        const uint4 v = __ldg(row + j);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float p = __uint_as_float(w[i] << 16), q = __uint_as_float(w[i] & 0xffff0000u);
+          ss = fmaf(p, p, ss);
+          ss = fmaf(q, q, ss);
+        }
+      }
+      ss = dec_warp_sum(ss);
+      if (lane == 0) s_r[warp] = 1.0f / sqrtf(ss / (float)a.d + a.eps);
+    }
+    __syncthreads();
+  }
+  auto input8 = [&](int t, int v) {  // vector v of token t's (normalised) row
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(a.x + (int64_t)t * a.d) + v);
+    return a.gamma ? dec_norm8(x, __ldg(gam + v), s_r[t]) : x;
+  };
+  // partial logits: units of 16 experts and a slice of d
+  const int tiles = (a.E + 15) >> 4;
+  const int nch = (a.d + 31) >> 5;
+  const int per = (nch + a.splits - 1) / a.splits;
+  for (int u = blockIdx.x; u < tiles * a.splits; u += gridDim.x) {
+    const int et = u % tiles, sp = u / tiles;
+    const bool ok0 = et * 16 + g < a.E, ok8 = et * 16 + g + 8 < a.E;
+    const uint4* w0 = reinterpret_cast<const uint4*>(a.w_router + (int64_t)(et * 16 + g) * a.d);
+    const uint4* w8 = w0 + a.d;  // eight rows of d / 8 vectors
+    float acc[NB][4];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[nb][i] = 0.f;
+    const int k1 = min(nch, (sp + 1) * per);
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 2
+    for (int kc = sp * per + warp; kc < k1; kc += kDecodeWarps) {
+      const int v = kc * 4 + c;
+      const bool kok = v * 8 < a.d;
+      const uint4 l = kok && ok0 ? __ldg(w0 + v) : z, h = kok && ok8 ? __ldg(w8 + v) : z;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const int t = nb * 8 + g;
+        const uint4 b = t < a.T && kok ? input8(t, v) : z;
+        mma_bf16(acc[nb], l.x, h.x, l.y, h.y, b.x, b.y);
+        mma_bf16(acc[nb], l.z, h.z, l.w, h.w, b.z, b.w);
+      }
+    }
+    __syncthreads();  // the previous unit's sums have been read
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) red[warp][(nb * 4 + i) * 32 + lane] = acc[nb][i];
+    __syncthreads();
+    for (int q = tid; q < NB * 128; q += kDecodeThreads) {
+      float v = 0.f;
+      for (int w = 0; w < kDecodeWarps; ++w) v += red[w][q];
+      const int ln = q & 31, i = (q >> 5) & 3, nb = q >> 7;
+      const int e = et * 16 + (ln >> 2) + (i >> 1) * 8, t = nb * 8 + (ln & 3) * 2 + (i & 1);
+      if (e < a.E && t < a.T) a.logits[((int64_t)sp * a.T + t) * a.E + e] = v;
+    }
+  }
+  // the products' input, and the shared expert's gate; the last warps of the grid first
+  const int gw = (gridDim.x - 1 - blockIdx.x) * kDecodeWarps + warp, gn = gridDim.x * kDecodeWarps;
+  if (DecW<W>::SCALED) {
+    const int nk = a.d >> 7;
+    for (int i = gw; i < a.T * nk; i += gn) {
+      const int t = i / nk, kb = i % nk;
+      const int at = kb * 128 + lane * 4;
+      const uint2 x = __ldg(reinterpret_cast<const uint2*>(a.x + (int64_t)t * a.d + at));
+      uint32_t w[2] = {x.x, x.y};
+      if (a.gamma) {
+        const uint2 gm = __ldg(reinterpret_cast<const uint2*>(a.gamma + at));
+        const uint4 n = dec_norm8(make_uint4(x.x, x.y, 0u, 0u), make_uint4(gm.x, gm.y, 0u, 0u), s_r[t]);
+        w[0] = n.x;
+        w[1] = n.y;
+      }
+      const float v[4] = {__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xffff0000u), __uint_as_float(w[1] << 16),
+                          __uint_as_float(w[1] & 0xffff0000u)};
+      dec_split<W>(v, a.xq + (int64_t)i * 256, a.xsc + kb * kDecodeMaxT + t, lane);
+    }
+  } else if (a.gamma) {
+    const int n8 = a.d >> 3;
+    for (int i = gw * 32 + lane; i < a.T * n8; i += gn * 32)
+      reinterpret_cast<uint4*>(a.xn)[i] = input8(i / n8, i % n8);
+  }
+  if (a.gate)
+    for (int t = gw; t < a.T; t += gn) {
+      float z = 0.f;
+#pragma unroll 4
+      for (int j = lane; j < a.d / 8; j += 32) {
+        const uint4 x = input8(t, j), w = __ldg(reinterpret_cast<const uint4*>(a.gate_w) + j);
+        const uint32_t p[4] = {x.x, x.y, x.z, x.w}, q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          z = fmaf(__uint_as_float(p[i] << 16), __uint_as_float(q[i] << 16), z);
+          z = fmaf(__uint_as_float(p[i] & 0xffff0000u), __uint_as_float(q[i] & 0xffff0000u), z);
+        }
+      }
+      z = dec_warp_sum(z);
+      if (lane == 0) a.gate[t] = 1.0f / (1.0f + expf(-z));
+    }
+}
+
+// -------------------------------------------------------------- experts
 // NB: blocks of 8 token columns (1 for T <= 8, 2 up to kDecodeMaxT).
 template <int W, int NB>
 __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a) {
-  constexpr int CH = DecW<W>::CH, BW = DecW<W>::BW;
+  constexpr int PC = DecW<W>::PC, BV = DecW<W>::BV, D = kDecStages;
   constexpr int RED = 2 * NB * 4 * 32;  // floats a warp hands to its team
-  extern __shared__ float red_all[];    // two buffers of kDecodeWarps * RED
+  extern __shared__ __align__(128) uint8_t dyn[];
   __shared__ DecShared s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
+  float* red_all = reinterpret_cast<float*>(dyn + kDecodeWarps * D * kDecStage);
 
-  // ---- 1. partial logits; x in the weights' K order
+  // ---- 1. routing, in every CTA alike (the logits in the rings' place)
   {
-    const int tiles = (a.E + 15) >> 4;
-    const int nch = (a.d + 31) >> 5;
-    const int per = (nch + a.splits - 1) / a.splits;
-    for (int u = blockIdx.x; u < tiles * a.splits; u += gridDim.x) {
-      const int et = u % tiles, sp = u / tiles;
-      const DecRows<kDecBf16> r =
-          dec_rows<kDecBf16>(reinterpret_cast<const uint8_t*>(a.w_router), nullptr, 0, a.E, a.d, et * 16, g, c);
-      float acc[NB][4];
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[nb][i] = 0.f;
-      const int k1 = min(nch, (sp + 1) * per);
-      for (int kc = sp * per + warp; kc < k1; kc += kDecodeWarps) {
-        const bool kok = kc * 32 + c * 8 < a.d;
-        DecFrag<kDecBf16> f;
-        uint32_t bw[NB][4];
-        dec_load<kDecBf16>(f, r, kc, kok);
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          const int t = nb * 8 + g;
-          dec_tok<kDecBf16>(bw[nb], t < a.T ? a.x + (int64_t)t * a.d + c * 8 : nullptr, kc, kok);
-        }
-        dec_mma<kDecBf16, NB>(acc, f, bw, ~0u);
-      }
-      __syncthreads();  // the previous unit's sums have been read
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) red_all[warp * RED + (nb * 4 + i) * 32 + lane] = acc[nb][i];
-      __syncthreads();
-      for (int q = tid; q < NB * 128; q += kDecodeThreads) {
-        float v = 0.f;
-        for (int w = 0; w < kDecodeWarps; ++w) v += red_all[w * RED + q];
-        const int ln = q & 31, i = (q >> 5) & 3, nb = q >> 7;
-        const int e = et * 16 + (ln >> 2) + (i >> 1) * 8, t = nb * 8 + (ln & 3) * 2 + (i & 1);
-        if (e < a.E && t < a.T) a.logits[((int64_t)sp * a.T + t) * a.E + e] = v;
-      }
+    float* lg = reinterpret_cast<float*>(dyn);
+    static_assert(kDecodeMaxT * 512 * 4 <= kDecodeWarps * D * kDecStage, "logits");
+    const int n = a.T * a.E;
+    for (int i = tid; i < n; i += kDecodeThreads) {
+      float v = a.bias ? __ldg(a.bias + i % a.E) : 0.f;
+#pragma unroll 4
+      for (int p = 0; p < a.splits; ++p) v += __ldcg(a.logits + (int64_t)p * n + i);
+      lg[i] = v;
     }
-    if (W != kDecBf16) {
-      const int n8 = a.T * (a.d >> 3);
-      for (int v = blockIdx.x * kDecodeThreads + tid; v < n8; v += gridDim.x * kDecodeThreads) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4*>(a.x) + v);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-        uint16_t o[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[dec_place<W>(e)] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-        reinterpret_cast<uint4*>(a.xs)[v] = make_uint4(o[0] | (uint32_t)o[1] << 16, o[2] | (uint32_t)o[3] << 16,
-                                                       o[4] | (uint32_t)o[5] << 16, o[6] | (uint32_t)o[7] << 16);
-      }
+    s.flag[tid] = 0;
+    if (tid < kDecodeMaxT * kMaxK) s.mask[tid] = 0;
+    for (int i = tid; i < kDecodeMaxT * kMaxK * kDecodeMaxT / 4; i += kDecodeThreads)
+      reinterpret_cast<uint32_t*>(&s.slot[0][0])[i] = 0xffffffffu;
+    __syncthreads();
+    if (warp < a.T) {
+      const float* l = lg + warp * a.E;
+      if (a.E <= 128) dec_topk<4>(l, a.E, a.k, warp, s);
+      else if (a.E <= 256) dec_topk<8>(l, a.E, a.k, warp, s);
+      else dec_topk<16>(l, a.E, a.k, warp, s);
+      __syncwarp();
+      if (lane < a.k) s.flag[s.ids[warp][lane]] = 1;
     }
-  }
-  if (!dec_grid_barrier(a.bar, 1, a.status, &s.ok)) return;
-
-  // ---- 2. routing, in every CTA alike
-  if (warp < a.T) {
-    if (a.E <= 128) dec_topk<4>(a, warp, s);
-    else if (a.E <= 256) dec_topk<8>(a, warp, s);
-    else dec_topk<16>(a, warp, s);
-  }
-  s.flag[tid] = 0;
-  if (tid < kDecodeMaxT * kMaxK) s.mask[tid] = 0;
-  for (int i = tid; i < kDecodeMaxT * kMaxK * kDecodeMaxT / 4; i += kDecodeThreads)
-    reinterpret_cast<uint32_t*>(&s.slot[0][0])[i] = 0xffffffffu;
-  __syncthreads();
-  const int npair = a.T * a.k;
-  if (tid < npair) s.flag[s.ids[tid / a.k][tid % a.k]] = 1;
-  __syncthreads();
-  {
+    __syncthreads();
     const int f = s.flag[tid];
     const unsigned m = __ballot_sync(0xffffffffu, f);
     if (lane == 0) s.wsum[warp] = __popc(m);
@@ -516,9 +629,13 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a
       s.rank[tid] = before;
     }
     if (tid == kDecodeThreads - 1) s.n_act = before + f;
+    __syncthreads();
   }
-  __syncthreads();
-  if (tid < npair) {
+  const int f_r = (a.I + 15) >> 4, f_s = (a.I_s + 15) >> 4;  // units of 16 features per expert
+  const int nch_d = (a.d + PC - 1) / PC;
+  const int nch_i = (a.I + PC - 1) / PC, nch_s = (a.I_s + PC - 1) / PC;
+  const int n_act = s.n_act;
+  if (tid < a.T * a.k) {
     const int t = tid / a.k, j = tid % a.k, e = s.ids[t][j];
     s.slot[s.rank[e]][t] = (int8_t)j;
     atomicOr(&s.mask[s.rank[e]], 1u << t);
@@ -527,37 +644,83 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a
       if (a.tw) a.tw[tid] = s.w[t][j];
     }
   }
-  const int f_r = (a.I + 15) >> 4, f_s = (a.I_s + 15) >> 4;  // units of 16 features per expert
-  const int nch_d = (a.d + CH - 1) / CH;
-  const int nch_i = (a.I + CH - 1) / CH, nch_s = (a.I_s + CH - 1) / CH;
+  for (int i = tid; i <= n_act; i += kDecodeThreads) {
+    const int64_t m = i < n_act ? s.act[i] : 0, block = (int64_t)(a.d >> 7) * (a.I >> 7);
+    s.wd[i] = i < n_act ? a.wd + DecW<W>::bytes(m * a.d * a.I) : a.sd;
+    s.sc[i] = i < n_act ? a.sc[2] + m * block * (W == kDecMx4 ? kMxTileBytes : 4) : a.sc[5];
+  }
   if (tid == 0) {
-    s.kw1 = team_warps(s.n_act * f_r + f_s, nch_d, gridDim.x);
-    s.kw2 = team_warps((a.d + 15) >> 4, s.n_act * nch_i + nch_s, gridDim.x);
+    s.kw1 = team_warps(n_act * f_r + f_s, nch_d, gridDim.x);
+    s.kw2 = team_warps((a.d + 15) >> 4, n_act * nch_i + nch_s, gridDim.x);
   }
   __syncthreads();
-  const int n_act = s.n_act;
-  const bf16* xin = W == kDecBf16 ? a.x : a.xs;
+  const uint32_t ring = smem_u32(dyn) + warp * (D * kDecStage);
+  int in_slot = 0, out_slot = 0;  // the stage to copy into, the stage to read
 
-  // ---- 3. gate/up and SwiGLU: units of 16 features, the shared expert's first
+  // ---- 2. gate/up and SwiGLU: units of 16 features, the shared expert's first
   {
     const int kw = s.kw1, team = warp / kw, tw = warp % kw, tpc = kDecodeWarps / kw;
-    const int units = f_s + n_act * f_r;
-    int buf = 0;
-    for (int u = blockIdx.x + gridDim.x * team; u < units; u += gridDim.x * tpc) {
+    const int units = f_s + n_act * f_r, step = gridDim.x * tpc;
+    const uint8_t* xin = DecW<W>::SCALED ? a.xq : reinterpret_cast<const uint8_t*>(a.gamma ? a.xn : a.x);
+    const int64_t xrow = (int64_t)a.d * 2;  // bytes of a token's row, as bf16 or as terms
+    const int64_t step8 = DecW<W>::bytes((int64_t)8 * a.d);
+    const uint32_t lane_at = dec_unit(g, c);
+    int iu = tw < nch_d ? blockIdx.x + gridDim.x * team : units, ik = tw;
+    const uint8_t *wg = nullptr, *wu = nullptr, *sp = nullptr;  // this lane's places in the next pieces
+    bool ok0 = true, ok8 = true;
+    auto enter = [&]() {
+      if (iu >= units) return;
+      const bool sh = iu < f_s;
+      const int n0 = (sh ? iu : (iu - f_s) % f_r) * 16, N = sh ? a.I_s : a.I;
+      const int64_t m = sh ? 0 : s.act[(iu - f_s) / f_r];
+      ok0 = W != kDecBf16 || n0 + g < N;
+      ok8 = W != kDecBf16 || n0 + g + 8 < N;
+      const int64_t at = DecW<W>::bytes(m * N * a.d) + dec_row_at<W>(n0 + (ok0 ? g : 0), a.d, c) + (int64_t)tw * 64;
+      wg = (sh ? a.sg : a.wg) + at;
+      wu = (sh ? a.su : a.wu) + at;
+      // lanes 0..15: gate's scales, 16..31: up's
+      const int64_t kt = a.d >> 7, mt = m * (N >> 7) * kt;
+      const uint8_t* sc = lane < 16 ? (sh ? a.sc[3] : a.sc[0]) : (sh ? a.sc[4] : a.sc[1]);
+      if (W == kDecMx4) sp = sc + mt * kMxTileBytes + mx4_scale_at(n0 + (lane & 15), (int64_t)tw * 4, kt);
+      if (W == kDecFp8) sp = sc + 4 * (mt + (n0 >> 7) * kt);
+    };
+    auto issue = [&]() {
+      if (iu < units) {
+        const uint32_t at = ring + in_slot * kDecStage;
+        const bool kok = W != kDecBf16 || ik * 32 + c * 8 < a.d;
+        dec_issue<W>(at + lane_at, wg, step8, kok && ok0, kok && ok8);
+        dec_issue<W>(at + kDecPiece + lane_at, wu, step8, kok && ok0, kok && ok8);
+        if (W == kDecMx4) dec_copy4(at + 2 * kDecPiece + lane * 4, sp);
+        if (W == kDecFp8 && (lane & 15) == 0) dec_copy4(at + 2 * kDecPiece + lane * 4, sp + (ik >> 1) * 4);
+        ik += kw;
+        wg += kw * 64;
+        wu += kw * 64;
+        if (W == kDecMx4) sp += kw * kMxTileBytes;
+        if (ik >= nch_d) {
+          ik = tw;
+          iu += step;
+          enter();
+        }
+      }
+      cp_async_commit();
+      in_slot = in_slot + 1 == D ? 0 : in_slot + 1;
+    };
+    enter();
+#pragma unroll 1
+    for (int i = 0; i < D; ++i) issue();
+    float* red = red_all + team * kw * RED;
+    for (int u = blockIdx.x + gridDim.x * team; u < units; u += step) {
       const bool sh = u < f_s;
       const int ga = sh ? 0 : (u - f_s) / f_r;
       const int n0 = (sh ? u : (u - f_s) % f_r) * 16;
       const int N = sh ? a.I_s : a.I;
-      const int64_t m = sh ? 0 : s.act[ga];
-      const DecRows<W> rg = dec_rows<W>(sh ? a.sg : a.wg, sh ? a.sc[3] : a.sc[0], m, N, a.d, n0, g, c);
-      const DecRows<W> ru = dec_rows<W>(sh ? a.su : a.wu, sh ? a.sc[4] : a.sc[1], m, N, a.d, n0, g, c);
-      const bf16* tok[NB];
+      const uint8_t* tok[NB];
       unsigned nbmask = 0;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         const int t = nb * 8 + g;
         const bool in = t < a.T && (sh || s.slot[ga][t] >= 0);
-        tok[nb] = in ? xin + (int64_t)t * a.d + dec_tok_off<W>(c) : nullptr;
+        tok[nb] = in ? xin + t * xrow : nullptr;
         nbmask |= (__any_sync(0xffffffffu, in) ? 1u : 0u) << nb;
       }
       float ag[NB][4], au[NB][4];
@@ -565,32 +728,28 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int i = 0; i < 4; ++i) ag[nb][i] = au[nb][i] = 0.f;
-      constexpr int U = W == kDecBf16 ? (NB == 1 ? 4 : 3) : (W == kDecMx4 && NB == 1 ? 2 : 1);
-      for (int kc = tw; kc < nch_d; kc += kw * U) {
-        DecFrag<W> fg[U], fu[U];
-        uint32_t bw[U][NB][BW];
+      for (int kc = tw; kc < nch_d; kc += kw) {
+        uint4 bw[NB][BV];
+        float2 xs[NB];
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const int q = kc + i * kw;
-          const bool kok = q < nch_d && (W != kDecBf16 || q * CH + c * 8 < a.d);
-          dec_load<W>(fg[i], rg, q, kok);
-          dec_load<W>(fu[i], ru, q, kok);
+        for (int nb = 0; nb < NB; ++nb) {
+          dec_tok<W>(bw[nb], tok[nb], kc, a.d, c);
+          xs[nb] = make_float2(1.f, 1.f);
+          if (DecW<W>::SCALED)
+            xs[nb] = __ldg(reinterpret_cast<const float2*>(a.xsc + (kc * PC >> 7) * kDecodeMaxT + nb * 8 + 2 * c));
         }
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const int q = kc + i * kw;
-          const bool kok = q < nch_d && (W != kDecBf16 || q * CH + c * 8 < a.d);
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb) dec_tok<W>(bw[i][nb], tok[nb], q, kok);
-        }
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          dec_mma<W, NB>(ag, fg[i], bw[i], nbmask);
-          dec_mma<W, NB>(au, fu[i], bw[i], nbmask);
-        }
+        cp_async_wait<D - 1>();
+        __syncwarp();
+        DecFrag fg, fu;
+        const uint32_t at = ring + out_slot * kDecStage;
+        dec_read<W>(fg, at, at + 2 * kDecPiece, lane);
+        dec_read<W>(fu, at + kDecPiece, at + 2 * kDecPiece + kDecScales, lane);
+        out_slot = out_slot + 1 == D ? 0 : out_slot + 1;
+        __syncwarp();  // the stage has been read
+        issue();
+        dec_mma<W, NB>(ag, fg, bw, xs, nbmask);
+        dec_mma<W, NB>(au, fu, bw, xs, nbmask);
       }
-      float* red = red_all + buf * (kDecodeWarps * RED) + (team * kw) * RED;
-      buf ^= 1;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -613,61 +772,166 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a
         if (j < 0) continue;
         const float w = sh ? (a.gate ? __ldg(a.gate + t) : 1.f) : s.w[t][j];
         const float hv = w * (vg / (1.f + __expf(-vg)) * vu);
-        a.h[((int64_t)t * (a.k + 1) + j) * a.ldh + dec_place<W>(f)] = __float2bfloat16_rn(hv);
+        a.h[((int64_t)t * (a.k + 1) + j) * a.ldh + f] = __float2bfloat16_rn(hv);
       }
+      if (kw > 1) team_sync(team, kw * 32);
+      else __syncwarp();
     }
   }
-  if (!dec_grid_barrier(a.bar, 2, a.status, &s.ok)) return;
 
-  // ---- 4. down projection: units of 16 outputs, K runs over every active expert
+  // ---- 3. down projection: units of 16 outputs, K runs over every active expert.
+  // Two pieces a stage; the first stages are copied before the barrier.
   {
     const int kw = s.kw2, team = warp / kw, tw = warp % kw, tpc = kDecodeWarps / kw;
-    const int units = (a.d + 15) >> 4;
+    const int units = (a.d + 15) >> 4, step = gridDim.x * tpc;
     const int total = n_act * nch_i + nch_s;
-    int buf = 0;
-    for (int u = blockIdx.x + gridDim.x * team; u < units; u += gridDim.x * tpc) {
+    // a piece (expert ga of the active ones, n_act: the shared one; piece kc), kw apart
+    struct Walk {
+      int ga, kc, left;
+    };
+    auto start = [&](Walk& w) {
+      w.ga = 0;
+      w.kc = tw;
+      w.left = total - tw;
+      while (w.ga < n_act && w.kc >= nch_i) {
+        w.kc -= nch_i;
+        ++w.ga;
+      }
+    };
+    auto next = [&](Walk& w) {
+      w.kc += kw;
+      w.left -= kw;
+      while (w.ga < n_act && w.kc >= nch_i) {
+        w.kc -= nch_i;
+        ++w.ga;
+      }
+    };
+    const int64_t step8_r = DecW<W>::bytes((int64_t)8 * a.I), step8_s = DecW<W>::bytes((int64_t)8 * a.I_s);
+    const uint32_t lane_at = dec_unit(g, c);
+    int iu = tw < total ? blockIdx.x + gridDim.x * team : units;
+    Walk iw;
+    // places of this lane in a routed and in the shared expert's matrix, and their scales
+    int64_t at_r = 0, at_s = 0, sc_r = 0, sc_s = 0;
+    bool ok0 = true, ok8 = true;
+    auto enter = [&]() {
+      start(iw);
+      const int n0 = iu * 16;
+      ok0 = W != kDecBf16 || n0 + g < a.d;
+      ok8 = W != kDecBf16 || n0 + g + 8 < a.d;
+      at_r = dec_row_at<W>(n0 + (ok0 ? g : 0), a.I, c);
+      at_s = dec_row_at<W>(n0 + (ok0 ? g : 0), a.I_s, c);
+      if (W == kDecMx4) {
+        sc_r = mx4_scale_at(n0 + (lane & 15), 0, a.I >> 7);
+        sc_s = mx4_scale_at(n0 + (lane & 15), 0, a.I_s >> 7);
+      }
+      if (W == kDecFp8) {
+        sc_r = 4 * (int64_t)(n0 >> 7) * (a.I >> 7);
+        sc_s = 4 * (int64_t)(n0 >> 7) * (a.I_s >> 7);
+      }
+    };
+    auto issue = [&]() {
+      if (iu < units) {
+        const uint32_t at = ring + in_slot * kDecStage;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (iw.left > 0) {
+            const bool sh = iw.ga >= n_act;
+            const bool kok = W != kDecBf16 || iw.kc * 32 + c * 8 < (sh ? a.I_s : a.I);
+            dec_issue<W>(at + i * kDecPiece + lane_at, s.wd[iw.ga] + (sh ? at_s : at_r) + iw.kc * 64,
+                         sh ? step8_s : step8_r, kok && ok0, kok && ok8);
+            const uint8_t* sp = s.sc[iw.ga] + (sh ? sc_s : sc_r);
+            if (W == kDecMx4 && (lane >> 4) == i) dec_copy4(at + 2 * kDecPiece + lane * 4, sp + iw.kc * kMxTileBytes);
+            if (W == kDecFp8 && lane == 16 * i) dec_copy4(at + 2 * kDecPiece + lane * 4, sp + (iw.kc >> 1) * 4);
+            next(iw);
+          }
+        if (iw.left <= 0) {
+          iu += step;
+          enter();
+        }
+      }
+      cp_async_commit();
+      in_slot = in_slot + 1 == D ? 0 : in_slot + 1;
+    };
+    enter();
+#pragma unroll 1
+    for (int i = 0; i < D; ++i) issue();
+    if (!dec_grid_barrier(a.bar, 1, a.status, &s.ok)) {
+      cp_async_wait<0>();
+      return;
+    }
+    const int ldt = a.ldh >> 7;
+    if (DecW<W>::SCALED) {
+      const int n = a.T * (a.k + 1) * ldt;
+      for (int i = blockIdx.x * kDecodeWarps + warp; i < n; i += gridDim.x * kDecodeWarps) {
+        const int r = i / ldt, kb = i % ldt;
+        if (kb * 128 >= (r % (a.k + 1) == a.k ? a.I_s : a.I)) continue;
+        const uint2 x = __ldcg(reinterpret_cast<const uint2*>(a.h + (int64_t)r * a.ldh + kb * 128 + lane * 4));
+        const float v[4] = {__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
+                            __uint_as_float(x.y & 0xffff0000u)};
+        dec_split<W>(v, a.hq + (int64_t)i * 256, a.hsc + i, lane);
+      }
+      if (!dec_grid_barrier(a.bar, 2, a.status, &s.ok)) {
+        cp_async_wait<0>();
+        return;
+      }
+    }
+    const uint8_t* hin = DecW<W>::SCALED ? a.hq : reinterpret_cast<const uint8_t*>(a.h);
+    const int64_t hrow = (int64_t)a.ldh * 2;
+    float* red = red_all + team * kw * RED;
+    for (int u = blockIdx.x + gridDim.x * team; u < units; u += step) {
       const int n0 = u * 16;
       float acc[NB][4];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[nb][i] = 0.f;
-      constexpr int U = W == kDecBf16 ? 4 : (W == kDecMx4 && NB == 1 ? 2 : 1);
-      for (int p = tw; p < total; p += kw * U) {
-        DecFrag<W> f[U];
-        uint32_t bw[U][NB][BW], member[U];
+      Walk w;
+      start(w);
+      while (w.left > 0) {
+        // both pieces' token data
+        uint4 bw[2][NB][BV];
+        float2 xs[2][NB];
+        uint32_t member[2];
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const int q = p + i * kw;
-          const bool in = q < total;
-          const int ga = in ? q / nch_i : 0;
-          const bool sh = in && ga >= n_act;
-          const int kc = sh ? q - n_act * nch_i : q - ga * nch_i;
+        for (int i = 0; i < 2; ++i) {
+          const bool in = w.left > 0, sh = w.ga >= n_act;
           const int K = sh ? a.I_s : a.I;
-          const bool kok = in && (W != kDecBf16 || kc * CH + c * 8 < K);
-          const DecRows<W> r = dec_rows<W>(sh ? a.sd : a.wd, sh ? a.sc[5] : a.sc[2], sh ? 0 : s.act[min(ga, n_act - 1)],
-                                           a.d, K, n0, g, c);
-          dec_load<W>(f[i], r, kc, kok);
-          member[i] = !in ? 0u : sh ? 0xffffu : s.mask[ga];
+          member[i] = !in ? 0u : sh ? 0xffffu : s.mask[w.ga];
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
             const int t = nb * 8 + g;
-            const int j = !kok || t >= a.T ? -1 : sh ? a.k : s.slot[ga][t];
-            const bf16* hp =
-                j >= 0 ? a.h + ((int64_t)t * (a.k + 1) + j) * a.ldh + dec_tok_off<W>(c) : nullptr;
-            dec_tok<W>(bw[i][nb], hp, kc, kok);
+            const int j = !in || t >= a.T ? -1 : sh ? a.k : s.slot[w.ga][t];
+            dec_tok<W>(bw[i][nb], j >= 0 ? hin + ((int64_t)t * (a.k + 1) + j) * hrow : nullptr, w.kc, K, c);
+            xs[i][nb] = make_float2(1.f, 1.f);
+            if (DecW<W>::SCALED) {  // lanes of group g hold token nb * 8 + g's; a lane wants columns 2c, 2c + 1
+              const float sv = j >= 0 ? a.hsc[((int64_t)t * (a.k + 1) + j) * ldt + (w.kc * PC >> 7)] : 0.f;
+              xs[i][nb].x = __shfl_sync(0xffffffffu, sv, 8 * c);
+              xs[i][nb].y = __shfl_sync(0xffffffffu, sv, 8 * c + 4);
+            }
           }
+          if (in) next(w);
         }
-        // the sum over experts takes an expert's part only for its own tokens: an
-        // infinity or a NaN in its weights reaches no other token
+        cp_async_wait<D - 1>();
+        __syncwarp();
+        DecFrag f[2];
+        const uint32_t at = ring + out_slot * kDecStage;
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
+        for (int i = 0; i < 2; ++i)
+          dec_read<W>(f[i], at + i * kDecPiece, at + 2 * kDecPiece + i * kDecScales, lane);
+        out_slot = out_slot + 1 == D ? 0 : out_slot + 1;
+        __syncwarp();  // the stage has been read
+        issue();
+        // the sum over experts takes an expert's part only for its own tokens: an
+        // infinity or a NaN in its weights reaches no other token (a second piece
+        // that does not exist has no members)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
           float part[NB][4];
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int r = 0; r < 4; ++r) part[nb][r] = 0.f;
-          dec_mma<W, NB>(part, f[i], bw[i], ~0u);
+          dec_mma<W, NB>(part, f[i], bw[i], xs[i], member[i] ? ~0u : 0u);
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -675,8 +939,6 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a
               if (member[i] >> (nb * 8 + 2 * c + (r & 1)) & 1u) acc[nb][r] += part[nb][r];
         }
       }
-      float* red = red_all + buf * (kDecodeWarps * RED) + (team * kw) * RED;
-      buf ^= 1;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -685,11 +947,13 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a
       else __syncwarp();
       for (int q = tw * 32 + lane; q < NB * 128; q += kw * 32) {
         float v = 0.f;
-        for (int w = 0; w < kw; ++w) v += red[w * RED + q];
+        for (int w2 = 0; w2 < kw; ++w2) v += red[w2 * RED + q];
         const int ln = q & 31, i = (q >> 5) & 3, nb = q >> 7;
         const int n = n0 + (ln >> 2) + (i >> 1) * 8, t = nb * 8 + (ln & 3) * 2 + (i & 1);
         if (n < a.d && t < a.T) a.y[(int64_t)t * a.d + n] = __float2bfloat16_rn(v);
       }
+      if (kw > 1) team_sync(team, kw * 32);
+      else __syncwarp();
     }
   }
 }

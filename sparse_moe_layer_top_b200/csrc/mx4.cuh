@@ -75,6 +75,32 @@ __device__ __forceinline__ float mx4_value(const mx4* codes, const uint8_t* scal
   return (q & 8u ? -a : a) * s;
 }
 
+// ---------------------------------------------------------------- E4M3 terms
+// The kernels that multiply 4-bit (or E4M3) weights by bf16 values take a value as
+// the sum of two E4M3 terms under one power-of-two scale per block of columns.
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {  // a in the low byte
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 e4m3x2_value(uint32_t q) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)q, __NV_E4M3);
+  return __half22float2(__half2(h));
+}
+
+// Scale byte of a block whose largest magnitude has the bits amax: the power of two
+// that puts it in (224, 448], the top of E4M3's range; at least 4, 255 for a NaN block.
+// amax = m * 2^(e - 127), and m <= 1.75 fits 448 = 1.75 * 2^8 under 2^(e - 127 - 8).
+__device__ __forceinline__ uint32_t mx_split_byte(uint32_t amax) {
+  const uint32_t e = amax >> 23;
+  if (e == 255u) return 255u;
+  const uint32_t b = e + ((amax & 0x7fffffu) > 0x600000u ? 1u : 0u);
+  return b < 12u ? 4u : b - 8u;
+}
+__device__ __forceinline__ float mx_split_inv(uint32_t b) {  // a NaN block multiplies by NaN: codes of NaN
+  return b == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float((254u - b) << 23);
+}
+
 // ---------------------------------------------------------------- quantise
 // Block scale of 32 values: with amax = m * 2^e, 1 <= m < 2, the scale is
 // 2^(e - 2), so that the largest value lands in [4, 8) and saturates above 6 (the

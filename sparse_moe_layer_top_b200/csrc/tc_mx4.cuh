@@ -80,8 +80,7 @@ struct Mx4Cfg {
 // col_tiles; prefix of the routed groups' column tiles), tile rows as the MMA's A
 // rows.  Rows in no group are left alone.
 //
-// Scale: the power of two that puts the block's largest value in (224, 448], the
-// top of E4M3's range; at least 2^-123, so that lo's byte (four less) exists.  A
+// Scale: mx_split_byte; at least 2^-123, so that lo's byte (four less) exists.  A
 // block holding an infinity or a NaN becomes NaN.
 // One warp per row, 8 values a lane (4 lanes a scale block), four loads in flight.
 struct MxSplitArgs {
@@ -99,24 +98,6 @@ struct MxSplitArgs {
 };
 constexpr int kMxSplitRows = 8;  // rows per block, one warp each
 
-__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {  // a in the low byte
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 e4m3x2_value(uint32_t q) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)q, __NV_E4M3);
-  return __half22float2(__half2(h));
-}
-
-// Scale byte of a 32-value block whose largest magnitude has the bits amax:
-// amax = m * 2^(e - 127), and m <= 1.75 fits 448 = 1.75 * 2^8 under 2^(e - 127 - 8).
-__device__ __forceinline__ uint32_t mx_split_byte(uint32_t amax) {
-  const uint32_t e = amax >> 23;
-  if (e == 255u) return 255u;
-  const uint32_t b = e + ((amax & 0x7fffffu) > 0x600000u ? 1u : 0u);
-  return b < 12u ? 4u : b - 8u;
-}
 __device__ __forceinline__ uint32_t mx_lo_byte(uint32_t b) { return b == 255u ? 255u : b - 4u; }
 // Two values under scale byte b -> their hi codes (low half) and lo codes (high half).
 __device__ __forceinline__ uint32_t mx_split2(float v0, float v1, float inv) {
@@ -125,10 +106,6 @@ __device__ __forceinline__ uint32_t mx_split2(float v0, float v1, float inv) {
   const float2 w = e4m3x2_value(h);
   return h | e4m3x2((a0 - w.x) * 16.f, (a1 - w.y) * 16.f) << 16;
 }
-__device__ __forceinline__ float mx_split_inv(uint32_t b) {  // a NaN block multiplies by NaN: codes of NaN
-  return b == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float((254u - b) << 23);
-}
-
 __global__ void __launch_bounds__(32 * kMxSplitRows) k_mx_split(MxSplitArgs p) {
   pdl_begin();  // after the previous kernel in the stream (programmatic launch)
   const int64_t r = (int64_t)blockIdx.x * kMxSplitRows + (threadIdx.x >> 5);

@@ -1,4 +1,4 @@
-"""The few-token forward (one kernel) against a plain 64-bit computation,
+"""The few-token forward against a plain 64-bit computation,
 element by element, with the error bound the kernel's roundings give.
 
 The bound, per element of y (u32 = 2^-24, u16 = 2^-8: half a step of fp32 and
@@ -9,6 +9,10 @@ bf16, relative):
   h = w * silu(g) * u inherits g's and u's (|silu'| <= 1.1), the fast exponential
   and the divisions (2^-18 together), the routing weight's own error, and one
   rounding to bf16; y its sum's, plus one rounding to bf16.
+With E4M3 weights x and h enter their products as two E4M3 terms under one scale
+per 128 columns: off by at most half of the second term's smallest spacing, 2^-10,
+where the largest of the 128 is above 224; with 4-bit weights as f16 under such a
+scale: half of its smallest spacing, 2^-25, where the largest is at least 2^14.
 The routing weight: a logit's error moves a softmax weight by at most twice
 that, relatively; expf and the division add 2^-20."""
 import numpy as np
@@ -82,15 +86,22 @@ def _reference(kw, ref, gate=None, out=None):
         w = torch.softmax(l.gather(1, ids), 1)
     w_rel = 2 * dl + 2.0 ** -20
 
+    def terms(v):
+        if p.w_dtype == 1:  # bf16 weights: v itself
+            return torch.zeros_like(v)
+        top = v.abs().unflatten(0, (-1, 128)).amax(1).repeat_interleave(128)
+        return top * (2.0 ** -10 / 224 if p.w_dtype == 2 else 2.0 ** -39)
+
     def expert(xt, f, wt, wrel):
         wg, wu, wd = f
         g, u = wg @ xt, wu @ xt
-        dg = (p.d + 8) * 2 * U32 * (wg.abs() @ xt.abs())
-        du = (p.d + 8) * 2 * U32 * (wu.abs() @ xt.abs())
+        dx = (p.d + 8) * 2 * U32 * xt.abs() + terms(xt)
+        dg, du = wg.abs() @ dx, wu.abs() @ dx
         s = g * torch.sigmoid(g)
         h = wt * s * u
         dh = wt * (1.1 * dg * u.abs() + (s.abs() + 1.1 * dg) * du)
         dh = dh + (h.abs() + dh) * (U16 + 2.0 ** -18 + wrel)
+        dh = dh + terms(h.abs() + dh)
         return wd @ h, wd.abs() @ dh, wd.abs() @ h.abs()
 
     y = torch.zeros_like(x)
