@@ -337,28 +337,29 @@ __device__ __forceinline__ void dec_split(const float (&v)[4], uint8_t* q, float
   }
 }
 
-// All CTAs of the cooperative grid have reached round `n` (1, 2, ..) of the
-// barrier.  Writes before it are visible to every thread after it.  Bounded as
-// every wait of the library; false: a CTA did not come.
-__device__ __forceinline__ bool dec_grid_barrier(unsigned* bar, unsigned n, unsigned* status, int* s_ok) {
+// Barrier of the cooperative grid, in two halves: writes before a CTA's arrival are
+// visible to every thread after the wait.  What a CTA can do without the others' writes
+// (starting the next copies) goes between; before the arrival it would hold up the
+// release.  Bounded as every wait of the library; false: a CTA did not come.
+__device__ __forceinline__ void dec_grid_arrive(unsigned* bar) {
   __syncthreads();
+  if (threadIdx.x == 0) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(bar) : "memory");
+}
+__device__ __forceinline__ bool dec_grid_wait(unsigned* bar, unsigned n, unsigned* status, int* s_ok) {
   if (threadIdx.x == 0) {
     const unsigned want = n * gridDim.x;
-    __threadfence();
-    atomicAdd(bar, 1u);
-    const long long t0 = clock64(), lim = wait_limit();
+    const long long t0 = clock64();
     int ok = 1;
-    for (;;) {
+    for (unsigned i = 1;; ++i) {
       unsigned v;
       asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(bar) : "memory");
       if (v >= want) break;
-      if (clock64() - t0 > lim) {
+      if ((i & 15u) == 0 && clock64() - t0 > wait_limit()) {
         atomicCAS(status, 0u, kStatusTimeoutBase | (kKernDecode << 8) | n);
         ok = 0;
         break;
       }
     }
-    __threadfence();
     *s_ok = ok;
   }
   __syncthreads();
@@ -367,12 +368,11 @@ __device__ __forceinline__ bool dec_grid_barrier(unsigned* bar, unsigned n, unsi
 
 // Warps per team for `units` units of `chunks` K chunks: the fewest rounds of
 // chunks, a split costing about one chunk for the reduction.
-__device__ __forceinline__ int team_warps(int units, int chunks, int grid) {
-  int best = 1;
-  int64_t cost = INT64_MAX;
-  for (int kw = 1; kw <= kDecodeWarps; kw *= 2) {
-    const int64_t teams = (int64_t)grid * (kDecodeWarps / kw);
-    const int64_t c = cdiv(units, teams) * (cdiv(chunks, kw) + (kw > 1 ? 1 : 0));
+__device__ __forceinline__ int team_warps(unsigned units, unsigned chunks, unsigned grid) {
+  unsigned best = 1, cost = ~0u;
+  for (unsigned kw = 1; kw <= kDecodeWarps; kw *= 2) {
+    const unsigned teams = grid * (kDecodeWarps / kw);
+    const unsigned c = (units + teams - 1) / teams * ((chunks + kw - 1) / kw + (kw > 1 ? 1 : 0));
     if (c < cost) {
       cost = c;
       best = kw;
@@ -634,6 +634,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a
   const int f_r = (a.I + 15) >> 4, f_s = (a.I_s + 15) >> 4;  // units of 16 features per expert
   const int nch_d = (a.d + PC - 1) / PC;
   const int nch_i = (a.I + PC - 1) / PC, nch_s = (a.I_s + PC - 1) / PC;
+  const int nst_i = (nch_i + 1) >> 1, nst_s = (nch_s + 1) >> 1;  // down projection: stages of two pieces
   const int n_act = s.n_act;
   if (tid < a.T * a.k) {
     const int t = tid / a.k, j = tid % a.k, e = s.ids[t][j];
@@ -649,10 +650,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a
     s.wd[i] = i < n_act ? a.wd + DecW<W>::bytes(m * a.d * a.I) : a.sd;
     s.sc[i] = i < n_act ? a.sc[2] + m * block * (W == kDecMx4 ? kMxTileBytes : 4) : a.sc[5];
   }
-  if (tid == 0) {
-    s.kw1 = team_warps(n_act * f_r + f_s, nch_d, gridDim.x);
-    s.kw2 = team_warps((a.d + 15) >> 4, n_act * nch_i + nch_s, gridDim.x);
-  }
+  if (tid == kDecodeThreads - 1) s.kw1 = team_warps(n_act * f_r + f_s, nch_d, gridDim.x);
+  if (tid == kDecodeThreads - 33) s.kw2 = team_warps((a.d + 15) >> 4, n_act * nst_i + nst_s, gridDim.x);
   __syncthreads();
   const uint32_t ring = smem_u32(dyn) + warp * (D * kDecStage);
   int in_slot = 0, out_slot = 0;  // the stage to copy into, the stage to read
@@ -779,74 +778,60 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a
     }
   }
 
-  // ---- 3. down projection: units of 16 outputs, K runs over every active expert.
-  // Two pieces a stage; the first stages are copied before the barrier.
+  dec_grid_arrive(a.bar);
+
+  // ---- 3. down projection: units of 16 outputs, K runs over every active expert,
+  // two consecutive pieces of one expert a stage; a warp of a team takes a contiguous
+  // range of the stages.  The first stages are copied before the barrier.
   {
     const int kw = s.kw2, team = warp / kw, tw = warp % kw, tpc = kDecodeWarps / kw;
     const int units = (a.d + 15) >> 4, step = gridDim.x * tpc;
-    const int total = n_act * nch_i + nch_s;
-    // a piece (expert ga of the active ones, n_act: the shared one; piece kc), kw apart
-    struct Walk {
-      int ga, kc, left;
-    };
-    auto start = [&](Walk& w) {
-      w.ga = 0;
-      w.kc = tw;
-      w.left = total - tw;
-      while (w.ga < n_act && w.kc >= nch_i) {
-        w.kc -= nch_i;
-        ++w.ga;
-      }
-    };
-    auto next = [&](Walk& w) {
-      w.kc += kw;
-      w.left -= kw;
-      while (w.ga < n_act && w.kc >= nch_i) {
-        w.kc -= nch_i;
-        ++w.ga;
-      }
-    };
-    const int64_t step8_r = DecW<W>::bytes((int64_t)8 * a.I), step8_s = DecW<W>::bytes((int64_t)8 * a.I_s);
+    const int total = n_act * nst_i + nst_s, per = (total + kw - 1) / kw;
+    const int p0 = tw * per, count = min(per, total - p0);  // this warp's stages of a unit (none: count <= 0)
+    const int ga0 = min(p0 / nst_i, n_act), ks0 = p0 - ga0 * nst_i;
     const uint32_t lane_at = dec_unit(g, c);
-    int iu = tw < total ? blockIdx.x + gridDim.x * team : units;
-    Walk iw;
-    // places of this lane in a routed and in the shared expert's matrix, and their scales
-    int64_t at_r = 0, at_s = 0, sc_r = 0, sc_s = 0;
+    // the next stage to copy: unit, expert (n_act: the shared one), stage in the expert
+    int iu = count > 0 ? blockIdx.x + gridDim.x * team : units, iga = 0, iks = 0, ileft = 0;
+    const uint8_t *wp = nullptr, *sp = nullptr;  // this lane's places
+    int64_t step8 = 0;
     bool ok0 = true, ok8 = true;
+    auto expert = [&]() {
+      const int K = iga < n_act ? a.I : a.I_s, n0 = iu * 16;
+      step8 = DecW<W>::bytes((int64_t)8 * K);
+      wp = s.wd[iga] + DecW<W>::bytes((int64_t)(n0 + (ok0 ? g : 0)) * K) + c * 16 + iks * 128;
+      if (W == kDecMx4) sp = s.sc[iga] + mx4_scale_at(n0 + (lane & 15), (int64_t)(2 * iks + (lane >> 4)) * 4, K >> 7);
+      if (W == kDecFp8) sp = s.sc[iga] + 4 * ((int64_t)(n0 >> 7) * (K >> 7) + iks);
+    };
     auto enter = [&]() {
-      start(iw);
-      const int n0 = iu * 16;
-      ok0 = W != kDecBf16 || n0 + g < a.d;
-      ok8 = W != kDecBf16 || n0 + g + 8 < a.d;
-      at_r = dec_row_at<W>(n0 + (ok0 ? g : 0), a.I, c);
-      at_s = dec_row_at<W>(n0 + (ok0 ? g : 0), a.I_s, c);
-      if (W == kDecMx4) {
-        sc_r = mx4_scale_at(n0 + (lane & 15), 0, a.I >> 7);
-        sc_s = mx4_scale_at(n0 + (lane & 15), 0, a.I_s >> 7);
-      }
-      if (W == kDecFp8) {
-        sc_r = 4 * (int64_t)(n0 >> 7) * (a.I >> 7);
-        sc_s = 4 * (int64_t)(n0 >> 7) * (a.I_s >> 7);
-      }
+      if (iu >= units) return;
+      ok0 = W != kDecBf16 || iu * 16 + g < a.d;
+      ok8 = W != kDecBf16 || iu * 16 + g + 8 < a.d;
+      iga = ga0;
+      iks = ks0;
+      ileft = count;
+      expert();
     };
     auto issue = [&]() {
       if (iu < units) {
         const uint32_t at = ring + in_slot * kDecStage;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (iw.left > 0) {
-            const bool sh = iw.ga >= n_act;
-            const bool kok = W != kDecBf16 || iw.kc * 32 + c * 8 < (sh ? a.I_s : a.I);
-            dec_issue<W>(at + i * kDecPiece + lane_at, s.wd[iw.ga] + (sh ? at_s : at_r) + iw.kc * 64,
-                         sh ? step8_s : step8_r, kok && ok0, kok && ok8);
-            const uint8_t* sp = s.sc[iw.ga] + (sh ? sc_s : sc_r);
-            if (W == kDecMx4 && (lane >> 4) == i) dec_copy4(at + 2 * kDecPiece + lane * 4, sp + iw.kc * kMxTileBytes);
-            if (W == kDecFp8 && lane == 16 * i) dec_copy4(at + 2 * kDecPiece + lane * 4, sp + (iw.kc >> 1) * 4);
-            next(iw);
-          }
-        if (iw.left <= 0) {
+        const int K = iga < n_act ? a.I : a.I_s, nch = iga < n_act ? nch_i : nch_s;
+        const bool two = 2 * iks + 1 < nch;
+        const bool k0 = W != kDecBf16 || iks * 64 + c * 8 < K, k1 = W != kDecBf16 || iks * 64 + 32 + c * 8 < K;
+        dec_issue<W>(at + lane_at, wp, step8, k0 && ok0, k0 && ok8);
+        if (two) dec_issue<W>(at + kDecPiece + lane_at, wp + 64, step8, k1 && ok0, k1 && ok8);
+        if (W == kDecMx4 && (two || lane < 16)) dec_copy4(at + 2 * kDecPiece + lane * 4, sp);
+        if (W == kDecFp8 && (lane & 15) == 0) dec_copy4(at + 2 * kDecPiece + lane * 4, sp);
+        wp += 128;
+        sp += W == kDecMx4 ? 2 * kMxTileBytes : 4;
+        if (--ileft == 0) {
           iu += step;
           enter();
+        } else if (iga < n_act && ++iks == nst_i) {
+          ++iga;
+          iks = 0;
+          expert();
+        } else if (iga == n_act) {
+          ++iks;
         }
       }
       cp_async_commit();
@@ -855,7 +840,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a
     enter();
 #pragma unroll 1
     for (int i = 0; i < D; ++i) issue();
-    if (!dec_grid_barrier(a.bar, 1, a.status, &s.ok)) {
+    if (!dec_grid_wait(a.bar, 1, a.status, &s.ok)) {
       cp_async_wait<0>();
       return;
     }
@@ -870,7 +855,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a
                             __uint_as_float(x.y & 0xffff0000u)};
         dec_split<W>(v, a.hq + (int64_t)i * 256, a.hsc + i, lane);
       }
-      if (!dec_grid_barrier(a.bar, 2, a.status, &s.ok)) {
+      dec_grid_arrive(a.bar);
+      if (!dec_grid_wait(a.bar, 2, a.status, &s.ok)) {
         cp_async_wait<0>();
         return;
       }
@@ -885,59 +871,71 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[nb][i] = 0.f;
-      Walk w;
-      start(w);
-      while (w.left > 0) {
-        // both pieces' token data
-        uint4 bw[2][NB][BV];
-        float2 xs[2][NB];
-        uint32_t member[2];
+      int ga = ga0, ks = ks0, left = count;
+      while (left > 0) {  // an expert's stages
+        const bool sh = ga >= n_act;
+        const int K = sh ? a.I_s : a.I, nch = sh ? nch_s : nch_i;
+        const int k1 = min(ks + left, sh ? nst_s : nst_i);
+        const uint32_t member = sh ? 0xffffu : s.mask[ga];
+        const uint8_t* tok[NB];
+        const float* tsc[NB];
+        unsigned nbmask = 0;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const bool in = w.left > 0, sh = w.ga >= n_act;
-          const int K = sh ? a.I_s : a.I;
-          member[i] = !in ? 0u : sh ? 0xffffu : s.mask[w.ga];
+        for (int nb = 0; nb < NB; ++nb) {
+          const int t = nb * 8 + g;
+          const int j = t >= a.T ? -1 : sh ? a.k : s.slot[ga][t];
+          const int64_t r = (int64_t)t * (a.k + 1) + j;
+          tok[nb] = j >= 0 ? hin + r * hrow : nullptr;
+          tsc[nb] = j >= 0 ? a.hsc + r * ldt : nullptr;
+          nbmask |= (member >> (8 * nb) & 0xffu ? 1u : 0u) << nb;
+        }
+        left -= k1 - ks;
+        // the sum over experts takes an expert's part only for its own tokens: an
+        // infinity or a NaN in its weights reaches no other token
+        float part[NB][4];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) part[nb][r] = 0.f;
+        for (; ks < k1; ++ks) {
+          uint4 bw[2][NB][BV];
+          float2 xs[2][NB];
+          const bool two = 2 * ks + 1 < nch;
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
-            const int t = nb * 8 + g;
-            const int j = !in || t >= a.T ? -1 : sh ? a.k : s.slot[w.ga][t];
-            dec_tok<W>(bw[i][nb], j >= 0 ? hin + ((int64_t)t * (a.k + 1) + j) * hrow : nullptr, w.kc, K, c);
-            xs[i][nb] = make_float2(1.f, 1.f);
+            dec_tok<W>(bw[0][nb], tok[nb], 2 * ks, K, c);
+            dec_tok<W>(bw[1][nb], two ? tok[nb] : nullptr, 2 * ks + 1, K, c);
+            xs[0][nb] = xs[1][nb] = make_float2(1.f, 1.f);
             if (DecW<W>::SCALED) {  // lanes of group g hold token nb * 8 + g's; a lane wants columns 2c, 2c + 1
-              const float sv = j >= 0 ? a.hsc[((int64_t)t * (a.k + 1) + j) * ldt + (w.kc * PC >> 7)] : 0.f;
-              xs[i][nb].x = __shfl_sync(0xffffffffu, sv, 8 * c);
-              xs[i][nb].y = __shfl_sync(0xffffffffu, sv, 8 * c + 4);
+              float v0 = 0.f, v1 = 0.f;
+              if (tok[nb]) {
+                v0 = tsc[nb][2 * ks * PC >> 7];
+                if (W == kDecMx4 && two) v1 = tsc[nb][2 * ks + 1];
+              }
+              xs[0][nb] = make_float2(__shfl_sync(0xffffffffu, v0, 8 * c), __shfl_sync(0xffffffffu, v0, 8 * c + 4));
+              xs[1][nb] = W == kDecMx4 ? make_float2(__shfl_sync(0xffffffffu, v1, 8 * c), __shfl_sync(0xffffffffu, v1, 8 * c + 4))
+                                       : xs[0][nb];
             }
           }
-          if (in) next(w);
+          cp_async_wait<D - 1>();
+          __syncwarp();
+          DecFrag f0, f1;
+          const uint32_t at = ring + out_slot * kDecStage;
+          dec_read<W>(f0, at, at + 2 * kDecPiece, lane);
+          dec_read<W>(f1, at + kDecPiece, at + 2 * kDecPiece + kDecScales, lane);
+          out_slot = out_slot + 1 == D ? 0 : out_slot + 1;
+          __syncwarp();  // the stage has been read
+          issue();
+          dec_mma<W, NB>(part, f0, bw[0], xs[0], nbmask);
+          if (two) dec_mma<W, NB>(part, f1, bw[1], xs[1], nbmask);
         }
-        cp_async_wait<D - 1>();
-        __syncwarp();
-        DecFrag f[2];
-        const uint32_t at = ring + out_slot * kDecStage;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          dec_read<W>(f[i], at + i * kDecPiece, at + 2 * kDecPiece + i * kDecScales, lane);
-        out_slot = out_slot + 1 == D ? 0 : out_slot + 1;
-        __syncwarp();  // the stage has been read
-        issue();
-        // the sum over experts takes an expert's part only for its own tokens: an
-        // infinity or a NaN in its weights reaches no other token (a second piece
-        // that does not exist has no members)
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float part[NB][4];
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) part[nb][r] = 0.f;
-          dec_mma<W, NB>(part, f[i], bw[i], xs[i], member[i] ? ~0u : 0u);
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              if (member[i] >> (nb * 8 + 2 * c + (r & 1)) & 1u) acc[nb][r] += part[nb][r];
-        }
+          for (int r = 0; r < 4; ++r)
+            if (member >> (nb * 8 + 2 * c + (r & 1)) & 1u) acc[nb][r] += part[nb][r];
+        ++ga;
+        ks = 0;
       }
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
