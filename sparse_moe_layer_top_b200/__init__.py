@@ -150,7 +150,7 @@ def _need(t, name, n, dtypes, row=None):
         raise ValueError("%s: element type %s, expected %s" % (name, t.dtype, " or ".join(map(str, dtypes))))
     if t.numel() < n:
         raise ValueError("%s: %d elements, the problem needs %d" % (name, t.numel(), n))
-    if row is not None and t.dim() >= 2 and t.shape[-1] != row:
+    if row is not None and t.dim() >= 2 and t.size(-1) != row:
         raise ValueError("%s: rows of %d elements, expected %d" % (name, t.shape[-1], row))
 
 
@@ -183,7 +183,7 @@ def _ptr(t):
         raise ValueError("tensor must be on a CUDA device")
     if not t.is_contiguous():
         raise ValueError("tensor must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _device(stream=None, **tensors):
@@ -191,30 +191,49 @@ def _device(stream=None, **tensors):
     given stream must belong to it.  Raises ValueError naming the tensors
     otherwise -- the library would launch on the current device with
     another device's pointers."""
-    devs = {}
-    for name, t in tensors.items():
+    first = index = None
+    same = True
+    for t in tensors.values():
         if t is not None:
-            devs.setdefault(t.device, []).append(name)
-    if len(devs) > 1:
-        raise ValueError("tensors on different devices: " +
-                         "; ".join("%s on %s" % (", ".join(n), d) for d, n in devs.items()))
-    dev = next(iter(devs), None)
+            i = t.get_device()
+            if first is None:
+                first, index = t, i
+            same = same and i == index and i >= 0
+    if not same:  # (or not on CUDA devices)
+        devs = {}
+        for name, t in tensors.items():
+            if t is not None:
+                devs.setdefault(t.device, []).append(name)
+        if len(devs) > 1:
+            raise ValueError("tensors on different devices: " +
+                             "; ".join("%s on %s" % (", ".join(n), d) for d, n in devs.items()))
+    dev = None if first is None else first.device
     if stream is not None and dev is not None and dev.type == "cuda" and stream.device != dev:
         raise ValueError("stream on %s, tensors on %s" % (stream.device, dev))
     return dev
 
 
+_NOTHING = contextlib.nullcontext()
+
+
 def _current(dev):
     """A context in which `dev` is the current CUDA device (nothing to do
     for a non-CUDA device: the pointer step rejects its tensors)."""
-    if dev is not None and dev.type == "cuda":
+    if dev is not None and dev.type == "cuda" and dev.index != torch.cuda.current_device():
         return torch.cuda.device(dev)
-    return contextlib.nullcontext()
+    return _NOTHING
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    """Handle of the stream, by default torch's current one on the current device."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None and torch.cuda.is_initialized():  # without building a Stream object (3 us)
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _act(prob):
@@ -283,7 +302,7 @@ def profile_read(max_launches=4096):
 def _alloc(stream):
     """A context in which new tensors belong to `stream`, the stream that uses
     them first (nothing to do for None, the current one)."""
-    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+    return torch.cuda.stream(stream) if stream is not None else _NOTHING
 
 
 def _ws(nbytes, device, ws):
@@ -602,7 +621,8 @@ def _decode(prob, x, w_router, bias, wg, wu, wd, s_wg, s_wu, s_wd, scales, norm_
     with _current(cur), _alloc(stream):
         if y is None:
             y = torch.empty((prob.T, prob.d), dtype=_act(prob), device=x.device)
-        ws = _ws(decode_workspace_size(prob), x.device, ws)
+        if ws is None:
+            ws = _ws(decode_workspace_size(prob), x.device, None)
         opt = BlockOptions(_ptr(norm_weight), float(norm_eps), _ptr(shared_gate))
         _check(lib().moe_decode_forward(ctypes.byref(prob), ctypes.byref(opt), _ptr(x), _ptr(w_router), _ptr(bias),
                                         _ptr(wg), _ptr(wu), _ptr(wd), _ptr(s_wg), _ptr(s_wu), _ptr(s_wd),
