@@ -368,17 +368,16 @@ __device__ __forceinline__ bool dec_grid_wait(unsigned* bar, unsigned n, unsigne
 
 // Warps per team for `units` units of `chunks` K chunks: the fewest rounds of
 // chunks, a split costing about one chunk for the reduction.
+// One warp; every lane returns it (lane i weighs 2^i warps).
 __device__ __forceinline__ int team_warps(unsigned units, unsigned chunks, unsigned grid) {
-  unsigned best = 1, cost = ~0u;
-  for (unsigned kw = 1; kw <= kDecodeWarps; kw *= 2) {
-    const unsigned teams = grid * (kDecodeWarps / kw);
-    const unsigned c = (units + teams - 1) / teams * ((chunks + kw - 1) / kw + (kw > 1 ? 1 : 0));
-    if (c < cost) {
-      cost = c;
-      best = kw;
-    }
+  const unsigned lane = threadIdx.x & 31;
+  unsigned key = ~0u;
+  if (1u << lane <= (unsigned)kDecodeWarps) {
+    const unsigned teams = grid * (kDecodeWarps >> lane);
+    const unsigned cost = (units + teams - 1) / teams * (((chunks + (1u << lane) - 1) >> lane) + (lane > 0 ? 1 : 0));
+    key = min(cost, ~0u >> 3) << 3 | lane;  // (of equal costs the fewest warps)
   }
-  return best;
+  return 1 << (__reduce_min_sync(0xffffffffu, key) & 7u);
 }
 
 __device__ __forceinline__ void team_sync(int team, int threads) {
@@ -397,10 +396,16 @@ struct DecShared {
   // down projection: the active experts' (then the shared expert's) matrices and scales
   const uint8_t* wd[kDecodeMaxT * kMaxK + 1];
   const uint8_t* sc[kDecodeMaxT * kMaxK + 1];
-  int n_act, kw1, kw2, ok;
+  int n_act, ok;
 };
 
-// Top k of one token's logits (l) by one warp: k rounds of (largest key, lowest
+__device__ __forceinline__ float dec_warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Top k of one token's logits by one warp: k rounds of (largest key, lowest
 // expert holding it).  Keys order as the logits; NaN sorts below every number.
 template <int NPL>
 __device__ __forceinline__ void dec_topk(const float* logits, int E, int k, int t, DecShared& s) {
@@ -417,8 +422,7 @@ __device__ __forceinline__ void dec_topk(const float* logits, int E, int k, int 
     if (l[i] != l[i]) q = 1u;
     key[i] = e < E ? q : 0u;
   }
-  float v0 = 0.f, den = 0.f, my_v = 0.f;
-  int my_e = 0;
+  unsigned my_e = 0;
   for (int j = 0; j < k; ++j) {
     uint32_t best = 0;
 #pragma unroll
@@ -429,20 +433,17 @@ __device__ __forceinline__ void dec_topk(const float* logits, int E, int k, int 
     for (int i = NPL - 1; i >= 0; --i)
       if (key[i] == top && lane + 32 * i < E) cand = lane + 32 * i;
     const unsigned e = __reduce_min_sync(0xffffffffu, cand);
-    const float v = logits[e];
 #pragma unroll
     for (int i = 0; i < NPL; ++i)
       if (e == (unsigned)(lane + 32 * i)) key[i] = 0u;
-    if (j == 0) v0 = v;
-    den += expf(v - v0);
-    if (lane == j) {
-      my_v = v;
-      my_e = (int)e;
-    }
+    if (lane == j) my_e = e;
   }
+  const float mine = lane < k ? logits[my_e] : 0.f, top = __shfl_sync(0xffffffffu, mine, 0);
+  const float p = lane < k ? expf(mine - top) : 0.f;
+  const float den = dec_warp_sum(p);
   if (lane < k) {
-    s.ids[t][lane] = my_e;
-    s.w[t][lane] = expf(my_v - v0) / den;
+    s.ids[t][lane] = (int)my_e;
+    s.w[t][lane] = p / den;
   }
 }
 
@@ -457,12 +458,6 @@ __device__ __forceinline__ uint4 dec_norm8(uint4 x, uint4 gamma, float r) {
                        __uint_as_float(a[i] & 0xffff0000u) * r * (1.0f + __uint_as_float(g[i] & 0xffff0000u)));
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
-__device__ __forceinline__ float dec_warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
 template <int W, int NB>
 __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode_route(const DecodeArgs a) {
   pdl_begin();  // after the previous kernel in the stream (programmatic launch)
@@ -650,15 +645,15 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a
     s.wd[i] = i < n_act ? a.wd + DecW<W>::bytes(m * a.d * a.I) : a.sd;
     s.sc[i] = i < n_act ? a.sc[2] + m * block * (W == kDecMx4 ? kMxTileBytes : 4) : a.sc[5];
   }
-  if (tid == kDecodeThreads - 1) s.kw1 = team_warps(n_act * f_r + f_s, nch_d, gridDim.x);
-  if (tid == kDecodeThreads - 33) s.kw2 = team_warps((a.d + 15) >> 4, n_act * nst_i + nst_s, gridDim.x);
+  const int kw1 = team_warps(n_act * f_r + f_s, nch_d, gridDim.x);
+  const int kw2 = team_warps((a.d + 15) >> 4, n_act * nst_i + nst_s, gridDim.x);
   __syncthreads();
   const uint32_t ring = smem_u32(dyn) + warp * (D * kDecStage);
   int in_slot = 0, out_slot = 0;  // the stage to copy into, the stage to read
 
   // ---- 2. gate/up and SwiGLU: units of 16 features, the shared expert's first
   {
-    const int kw = s.kw1, team = warp / kw, tw = warp % kw, tpc = kDecodeWarps / kw;
+    const int kw = kw1, team = warp / kw, tw = warp % kw, tpc = kDecodeWarps / kw;
     const int units = f_s + n_act * f_r, step = gridDim.x * tpc;
     const uint8_t* xin = DecW<W>::SCALED ? a.xq : reinterpret_cast<const uint8_t*>(a.gamma ? a.xn : a.x);
     const int64_t xrow = (int64_t)a.d * 2;  // bytes of a token's row, as bf16 or as terms
@@ -784,7 +779,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a
   // two consecutive pieces of one expert a stage; a warp of a team takes a contiguous
   // range of the stages.  The first stages are copied before the barrier.
   {
-    const int kw = s.kw2, team = warp / kw, tw = warp % kw, tpc = kDecodeWarps / kw;
+    const int kw = kw2, team = warp / kw, tw = warp % kw, tpc = kDecodeWarps / kw;
     const int units = (a.d + 15) >> 4, step = gridDim.x * tpc;
     const int total = n_act * nst_i + nst_s, per = (total + kw - 1) / kw;
     const int p0 = tw * per, count = min(per, total - p0);  // this warp's stages of a unit (none: count <= 0)
