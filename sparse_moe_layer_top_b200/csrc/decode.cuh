@@ -141,12 +141,13 @@ __device__ __forceinline__ uint32_t lds32(uint32_t at) {
 __device__ __forceinline__ void lds128(uint32_t (&r)[4], uint32_t at) {
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
 }
-// 16 bytes global -> shared past L1 (zeros where ok is false); 4 bytes.
+// 16 bytes global -> shared past L1 (zeros where ok is false), the rest of a 256-byte
+// piece of the row to L2 with them (four tokens on E4M3 weights 117 -> 111 us); 4 bytes.
 __device__ __forceinline__ void dec_copy16(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16u : 0u) : "memory");
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16u : 0u) : "memory");
 }
 __device__ __forceinline__ void dec_copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void dec_copy4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -461,18 +462,21 @@ __device__ __forceinline__ uint4 dec_norm8(uint4 x, uint4 gamma, float r) {
 template <int W, int NB>
 __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode_route(const DecodeArgs a) {
   pdl_begin();  // after the previous kernel in the stream (programmatic launch)
-  __shared__ float s_r[kDecodeMaxT];
+  __shared__ float s_r[kDecodeMaxT], s_part[kDecodeWarps];
   __shared__ float red[kDecodeWarps][NB * 128];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
   if (blockIdx.x == 0 && tid == 0) *a.bar = 0;
   const uint4* gam = reinterpret_cast<const uint4*>(a.gamma);
-  if (a.gamma) {  // 1 / rms of every token, in every CTA alike
-    if (warp < a.T) {
-      const uint4* row = reinterpret_cast<const uint4*>(a.x + (int64_t)warp * a.d);
-      float ss = 0.f;
-#pragma unroll 8
-      for (int j = lane; j < a.d / 8; j += 32) {
+  if (a.gamma) {  // 1 / rms of every token, in every CTA alike: the warps share the tokens out
+    int wpt = 16;  // warps of a token
+    while (wpt * a.T > kDecodeWarps) wpt >>= 1;
+    const int t = warp / wpt;
+    float ss = 0.f;
+    if (t < a.T) {
+      const uint4* row = reinterpret_cast<const uint4*>(a.x + (int64_t)t * a.d);
+#pragma unroll 4
+      for (int j = warp % wpt * 32 + lane; j < a.d / 8; j += wpt * 32) {
         const uint4 v = __ldg(row + j);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -483,7 +487,13 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode_route(const Decode
         }
       }
       ss = dec_warp_sum(ss);
-      if (lane == 0) s_r[warp] = 1.0f / sqrtf(ss / (float)a.d + a.eps);
+    }
+    if (lane == 0) s_part[warp] = ss;
+    __syncthreads();
+    if (tid < a.T) {
+      float v = 0.f;
+      for (int w = 0; w < wpt; ++w) v += s_part[tid * wpt + w];
+      s_r[tid] = 1.0f / sqrtf(v / (float)a.d + a.eps);
     }
     __syncthreads();
   }
@@ -558,11 +568,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode_route(const Decode
     for (int i = gw * 32 + lane; i < a.T * n8; i += gn * 32)
       reinterpret_cast<uint4*>(a.xn)[i] = input8(i / n8, i % n8);
   }
-  if (a.gate)
-    for (int t = gw; t < a.T; t += gn) {
+  if (a.gate)  // a CTA per token, from the grid's end
+    for (int t = gridDim.x - 1 - blockIdx.x; t < a.T; t += gridDim.x) {
       float z = 0.f;
-#pragma unroll 4
-      for (int j = lane; j < a.d / 8; j += 32) {
+      for (int j = tid; j < a.d / 8; j += kDecodeThreads) {
         const uint4 x = input8(t, j), w = __ldg(reinterpret_cast<const uint4*>(a.gate_w) + j);
         const uint32_t p[4] = {x.x, x.y, x.z, x.w}, q[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -572,7 +581,14 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode_route(const Decode
         }
       }
       z = dec_warp_sum(z);
-      if (lane == 0) a.gate[t] = 1.0f / (1.0f + expf(-z));
+      __syncthreads();  // s_part has been read
+      if (lane == 0) s_part[warp] = z;
+      __syncthreads();
+      if (tid == 0) {
+        float v = 0.f;
+        for (int w = 0; w < kDecodeWarps; ++w) v += s_part[w];
+        a.gate[t] = 1.0f / (1.0f + expf(-v));
+      }
     }
 }
 
