@@ -207,14 +207,16 @@ __device__ __forceinline__ uint32_t idesc_mx4(int N, int id) {
   return ((uint32_t)id << 4) | (0u << 7) | (5u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | (1u << 27) |
          ((uint32_t)id << 29);
 }
-// The accumulator's hi rows (even lanes) and lo rows (odd lanes) of 64 columns
-// (a: 0..31, b: 32..63) summed: the even lane gets columns 0..31 in a, the odd
-// lane 32..63.
-__device__ __forceinline__ void mx_sum_planes(uint32_t (&a)[32], const uint32_t (&b)[32], bool odd) {
+// The accumulator's hi rows (even lanes) and lo rows (odd lanes) of 32 columns summed:
+// of every 2 G columns the even lane gets the first G, the odd lane the others, so
+// that a 16-byte store of the two fills a 32-byte sector.
+template <int G>
+__device__ __forceinline__ void mx_sum_planes(const uint32_t (&a)[32], uint32_t* out, bool odd) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? a[j] : b[j], 1);
-    a[j] = __float_as_uint(__uint_as_float(odd ? b[j] : a[j]) + __uint_as_float(got));
+  for (int j = 0; j < 16; ++j) {
+    const uint32_t e = a[j / G * 2 * G + j % G], o = a[j / G * 2 * G + G + j % G];
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? e : o, 1);
+    out[j] = __float_as_uint(__uint_as_float(odd ? o : e) + __uint_as_float(got));
   }
 }
 __device__ __forceinline__ uint4 mx_bf16x8(const uint32_t* v, float w) {
@@ -463,7 +465,7 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
     // ------------------------------------------------ epilogue
     // Warps of lane quarter q = warp % 4 hold tokens 16 q .. 16 q + 15 (lane pairs);
     // the two of a quarter take half of the weight rows each.  After the planes are
-    // summed a lane has one token and 32 (SwiGLU) or 64 consecutive outputs.
+    // summed a lane has one token and 32 features (SwiGLU) or 64 outputs.
     const int q = warp & 3, eg = (warp - 2) >> 2;
     const bool odd = lane & 1;
     const int i = q * 32 + lane, jj = i >> 1;
@@ -484,67 +486,77 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
       acc_phase ^= 1;
       tc_fence_after();
       const bool work = q * 16 < t.rows - t.c0 && (!HALVES || t.n0 + eg * 128 < t.N);  // (uniform in the warp)
-      // SwiGLU: v0 the gate, v2 the up sums of this lane's 32 features; else v0 and v2
-      // the lane's 64 outputs
-      uint32_t v0[32], v2[32];
+      // the lane's sums.  SwiGLU: v the gate of 2 x 16 of 64 features, w2 their up; else
+      // v and w2 64 of 128 outputs, 8 of every 16
+      constexpr int G = HALVES ? 8 : 16;
+      uint32_t v[32], w2[32];
       if (work) {
         const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + (HALVES ? eg * 128 : eg * 64);
-        uint32_t v1[32];
-        tmem_ld32(tb, v0);
-        tmem_ld32(tb + (HALVES ? 64 : 32), v1);
-        tmem_wait_regs(v0);
-        tmem_wait_regs(v1);
-        mx_sum_planes(v0, v1, odd);
-        tmem_ld32(tb + (HALVES ? 32 : 128), v2);
-        tmem_ld32(tb + (HALVES ? 96 : 160), v1);
-        tmem_wait_regs(v2);
-        tmem_wait_regs(v1);
-        mx_sum_planes(v2, v1, odd);
+        uint32_t t0[32], t1[32];
+        tmem_ld32(tb, t0);
+        tmem_ld32(tb + 32, t1);
+        tmem_wait_regs(t0);
+        tmem_wait_regs(t1);
+        mx_sum_planes<G>(t0, v, odd);
+        mx_sum_planes<G>(t1, v + 16, odd);
+        tmem_ld32(tb + (HALVES ? 64 : 128), t0);
+        tmem_ld32(tb + (HALVES ? 96 : 160), t1);
+        tmem_wait_regs(t0);
+        tmem_wait_regs(t1);
+        mx_sum_planes<G>(t0, w2, odd);
+        mx_sum_planes<G>(t1, w2 + 16, odd);
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(tempty);
       if (!work) continue;
       if (EPI == kTcSwiGLU) {
-        uint32_t amax = 0, l8[8];
+        // 16 features each of two 32-feature blocks; the pair holds both blocks' other halves
+        uint32_t amax[2] = {0, 0};
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          v0[j] = __float_as_uint(silu_f32(__uint_as_float(v0[j])) * __uint_as_float(v2[j]));
-          amax = max(amax, v0[j] & 0x7fffffffu);
+          v[j] = __float_as_uint(silu_f32(__uint_as_float(v[j])) * __uint_as_float(w2[j]));
+          amax[j >> 4] = max(amax[j >> 4], v[j] & 0x7fffffffu);
         }
         // the activation enters the down product as two E4M3 terms, with no bf16
         // in between: hi and lo / 16 hold it to 2^-8 of its value, as bf16 would
-        const uint32_t b = mx_split_byte(amax);
-        const float inv = mx_split_inv(b);
+        uint32_t b[2];
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const uint32_t s0 = mx_split2(__uint_as_float(v0[j]), __uint_as_float(v0[j + 1]), inv);
-          const uint32_t s1 = mx_split2(__uint_as_float(v0[j + 2]), __uint_as_float(v0[j + 3]), inv);
-          v2[j / 4] = __byte_perm(s0, s1, 0x5410);
-          l8[j / 4] = __byte_perm(s0, s1, 0x7632);
+        for (int k = 0; k < 2; ++k) {
+          b[k] = mx_split_byte(max(amax[k], __shfl_xor_sync(0xffffffffu, amax[k], 1)));
+          const float inv = mx_split_inv(b[k]);
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            const uint32_t* x = v + 16 * k + j;
+            const uint32_t s0 = mx_split2(__uint_as_float(x[0]), __uint_as_float(x[1]), inv);
+            const uint32_t s1 = mx_split2(__uint_as_float(x[2]), __uint_as_float(x[3]), inv);
+            w2[4 * k + j / 4] = __byte_perm(s0, s1, 0x5410);
+            w2[8 + 4 * k + j / 4] = __byte_perm(s0, s1, 0x7632);
+          }
         }
         const int chunk = s_pre[t.g] / a.col_tiles + t.c0 / kNCH;
         if (!in || chunk > a.max_chunk) continue;
-        const int n = t.n0 + eg * 64 + (odd ? 32 : 0);
-        uint4* h = reinterpret_cast<uint4*>(a.hl_out + 2 * row * p.ldh + n);
-        uint4* l = reinterpret_cast<uint4*>(a.hl_out + (2 * row + 1) * p.ldh + n);
-        h[0] = make_uint4(v2[0], v2[1], v2[2], v2[3]);
-        h[1] = make_uint4(v2[4], v2[5], v2[6], v2[7]);
-        l[0] = make_uint4(l8[0], l8[1], l8[2], l8[3]);
-        l[1] = make_uint4(l8[4], l8[5], l8[6], l8[7]);
-        const int ih = 2 * jj;
-        uint8_t* s = a.sf_out + ((int64_t)chunk * (p.ldh / 128) + (n >> 7)) * kMxTileBytes + (ih & 31) * 16 +
-                     (ih >> 5) * 4 + ((n & 127) >> 5);
-        s[0] = (uint8_t)b;
-        s[16] = (uint8_t)mx_lo_byte(b);
+        const int n = t.n0 + eg * 64;
+        uint8_t* h = a.hl_out + 2 * row * p.ldh + n + (odd ? 16 : 0);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          *reinterpret_cast<uint4*>(h + 32 * k) = make_uint4(w2[4 * k], w2[4 * k + 1], w2[4 * k + 2], w2[4 * k + 3]);
+          *reinterpret_cast<uint4*>(h + p.ldh + 32 * k) =
+              make_uint4(w2[8 + 4 * k], w2[9 + 4 * k], w2[10 + 4 * k], w2[11 + 4 * k]);
+        }
+        // the two blocks' scale bytes: the even lane writes hi's (A row i), the odd lane lo's
+        uint8_t* sf = a.sf_out + ((int64_t)chunk * (p.ldh / 128) + (n >> 7)) * kMxTileBytes + (i & 31) * 16 +
+                      (i >> 5) * 4 + ((n & 127) >> 5);
+        *reinterpret_cast<uint16_t*>(sf) =
+            (uint16_t)(odd ? mx_lo_byte(b[0]) | mx_lo_byte(b[1]) << 8 : b[0] | b[1] << 8);
       } else {
         if (!in) continue;
-        const int n = t.n0 + eg * 128 + (odd ? 64 : 0);
+        const int n = t.n0 + eg * 128 + (odd ? 8 : 0);
         bf16* o = EPI == kTcSlotStore ? p.ys + dst * p.ldy + n : p.out + row * p.ldo + n;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) reinterpret_cast<uint4*>(o)[j] = mx_bf16x8(v0 + 8 * j, w);
+        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(o + 16 * j) = mx_bf16x8(v + 8 * j, w);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) reinterpret_cast<uint4*>(o)[4 + j] = mx_bf16x8(v2 + 8 * j, w);
+        for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(o + 64 + 16 * j) = mx_bf16x8(w2 + 8 * j, w);
       }
     }
   }
