@@ -515,7 +515,10 @@ __global__ void __launch_bounds__(Mx4Cfg::THREADS, 1)
         uint32_t amax[2] = {0, 0};
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          v[j] = __float_as_uint(silu_f32(__uint_as_float(v[j])) * __uint_as_float(w2[j]));
+          // (the fast division, good to two steps of fp32: with the exact one this epilogue
+          // held up the products of short K, 4096 tokens 205 us against 164)
+          const float z = __uint_as_float(v[j]);
+          v[j] = __float_as_uint(__fdividef(z, 1.f + __expf(-z)) * __uint_as_float(w2[j]));
           amax[j >> 4] = max(amax[j >> 4], v[j] & 0x7fffffffu);
         }
         // the activation enters the down product as two E4M3 terms, with no bf16
