@@ -134,6 +134,37 @@ def _check(status):
         raise MoEError(status, lib().moe_last_error_string().decode())
 
 
+_binding = False
+
+
+def _fast():
+    """The binding's C++ side (csrc/binding.cpp), which makes the regular calls of
+    the latency-bound entry points without the checks below; None when it is not
+    built or cannot be loaded -- the calls then go through Python, with the same results."""
+    global _binding
+    if _binding is False:
+        try:
+            from . import _moe_binding as m
+        except ImportError:
+            m = None
+        if m is not None:
+            L = lib()
+            m.bind(*(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
+                "moe_mx4_quantize", "moe_mx4_dequantize", "moe_expert_ffn", "moe_stage_workspace_size",
+                "moe_decode_workspace_size", "moe_decode_forward")))
+        _binding = m
+    return _binding
+
+
+def _fast_call(name, *args):
+    """A regular call's result, or None: this is not one (see _fast)."""
+    m = _binding if _binding is not False else _fast()
+    r = getattr(m, name)(*args) if m is not None else None
+    if r.__class__ is int:
+        _check(r)
+    return r
+
+
 _F32, _I32 = (torch.float32,), (torch.int32,)
 _ACT_TYPES = {F32: (torch.float32,), BF16: (torch.bfloat16,)}
 _W_TYPES = {F32: (torch.float32,), BF16: (torch.bfloat16,), FP8_E4M3_B128: (torch.float8_e4m3fn, torch.uint8),
@@ -359,6 +390,10 @@ def permute(prob, x, topk_ids, topk_w, ws=None, stream=None):
 
 def expert_ffn(prob, x_perm, offs, wg, wu, wd, s_wg=None, s_wu=None, s_wd=None, scales=None, y_perm=None,
                ws=None, stream=None):
+    if stream is None:
+        r = _fast_call("expert_ffn", prob, x_perm, offs, wg, wu, wd, s_wg, s_wu, s_wd, scales, y_perm, ws)
+        if r is not None:
+            return r
     a, Rp = _ACT_TYPES.get(prob.act_dtype), rows_total(prob)
     _need(x_perm, "x_perm", Rp * prob.d, a, prob.d)
     _need(offs, "offs", prob.E + 2, _I32)
@@ -524,6 +559,10 @@ def quantize_mx4(x, codes=None, scales=None, stream=None):
     multiple of 32) -> (codes uint8 [..., rows, cols / 2], scales uint8
     [..., ceil(rows / 128), ceil(cols / 128), 512]); the layouts and the
     rounding are those of moe_mx4_quantize in include/moe.h."""
+    if stream is None:
+        r = _fast_call("quantize", x, codes, scales)
+        if r is not None:
+            return r
     batch, rows, cols = _mx4_shape(x.shape)
     if x.dtype not in _MX4_FLOAT:
         raise ValueError("x: element type %s, expected torch.float32 or torch.bfloat16" % x.dtype)
@@ -546,6 +585,10 @@ def quantize_mx4(x, codes=None, scales=None, stream=None):
 
 def dequantize_mx4(codes, scales, out=None, dtype=torch.bfloat16, stream=None):
     """The values codes * scale of quantize_mx4's outputs, in bf16 or fp32 (exact)."""
+    if stream is None and dtype in _MX4_FLOAT:
+        r = _fast_call("dequantize", codes, scales, out, dtype is torch.float32)
+        if r is not None:
+            return r
     if codes.dtype != torch.uint8:
         raise ValueError("codes: element type %s, expected torch.uint8" % codes.dtype)
     shape = _mx4_shape(codes.shape) and tuple(codes.shape[:-1]) + (2 * codes.shape[-1],)
@@ -605,8 +648,13 @@ def decode_workspace_size(prob):
 def decode_forward(prob, x, w_router, bias, wg, wu, wd, s_wg=None, s_wu=None, s_wd=None, scales=None,
                    norm_weight=None, norm_eps=1e-6, shared_gate=None, y=None, topk_ids=None, topk_w=None, ws=None,
                    stream=None):
-    """block_forward for at most DECODE_MAX_T tokens in one kernel (two with the
-    norm or the gate): the latency form.  ws: decode_workspace_size bytes."""
+    """block_forward for at most DECODE_MAX_T tokens in two kernels: the latency
+    form.  ws: decode_workspace_size bytes."""
+    if stream is None:
+        r = _fast_call("decode", prob, x, w_router, bias, wg, wu, wd, s_wg, s_wu, s_wd, scales, norm_weight, norm_eps,
+                       shared_gate, y, topk_ids, topk_w, ws)
+        if r is not None:
+            return r
     _need_params(prob, w_router, bias, wg, wu, wd, s_wg, s_wu, s_wd, scales, norm_weight, shared_gate)
     _need_tokens(prob, x, y, topk_ids, topk_w)
     return _decode(prob, x, w_router, bias, wg, wu, wd, s_wg, s_wu, s_wd, scales, norm_weight, norm_eps, shared_gate,
@@ -633,7 +681,7 @@ def _decode(prob, x, w_router, bias, wg, wu, wd, s_wg, s_wu, s_wd, scales, norm_
 
 class MoELayer:
     """One block's weights plus a workspace sized for up to `max_tokens` tokens.
-    Calling it runs the fused forward; ``decode`` the one-kernel form for a few
+    Calling it runs the fused forward; ``decode`` the latency form for a few
     tokens, in a workspace of its own."""
 
     def __init__(self, d, E, k, I, I_s, w_router, wg, wu, wd, s_wg=None, s_wu=None, s_wd=None, bias=None,
@@ -671,7 +719,7 @@ class MoELayer:
                         shared_gate, y, topk_ids, topk_w, self.ws, stream, block)
 
     def decode(self, x, y=None, topk_ids=None, topk_w=None, stream=None):
-        """The block on x [T, d], T <= DECODE_MAX_T, in one kernel (decode_forward)."""
+        """The block on x [T, d], T <= DECODE_MAX_T, in the latency form (decode_forward)."""
         prob = self.problem(x.shape[0])
         _need_tokens(prob, x, y, topk_ids, topk_w)
         n = decode_workspace_size(prob)
