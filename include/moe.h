@@ -201,19 +201,24 @@ MOE_API moe_status moe_rmsnorm(const moe_problem* p, const void* x, const void* 
 
 /* The whole block for a few tokens (decode steps, speculated tokens): the
  * computation of moe_block_forward (same arguments; opt may be NULL) for
- * T <= 16 in one cooperative kernel, preceded by the prologue kernel when
- * opt asks for the norm or the shared gate.  Where moe_block_forward spends
- * five or six launches, this one's time is the active experts' weight bytes
- * plus about ten microseconds.  bf16 activations; BF16, FP8_E4M3_B128 or
- * MXFP4_B32 weights.  Sums are fp32 throughout: the SwiGLU activation, already
- * multiplied by the routing weight, is rounded to bf16 once, y once, and the
- * down projection is one sum over the token's experts, so results differ from
- * moe_block_forward's in rounding only; they are reproducible bit for bit.  An
- * infinity or a NaN in the weights of an expert reaches only the tokens routed
- * to it.  The kernel needs every SM of the device: it starts when earlier work
- * leaves them free.  ws: moe_decode_workspace_size() bytes, not shared with a
- * call that may run at the same time.  T > 16 or F32 activations:
- * MOE_ERR_UNSUPPORTED (use moe_block_forward). */
+ * T <= 16 in two kernels, the second a cooperative one.  Where
+ * moe_block_forward spends five to seven launches, this one's time is the active
+ * experts' weight bytes plus about fifteen microseconds.  bf16 activations;
+ * BF16, FP8_E4M3_B128 or MXFP4_B32 weights.  Sums are fp32 throughout.  The
+ * SwiGLU activation, already multiplied by the routing weight, enters the down
+ * projection rounded once: to bf16 (BF16 weights), to the sum of two E4M3 terms
+ * (E4M3 weights; x enters its products the same way) or to fp16 (4-bit
+ * weights; x too, exactly but for values 2^-31 of its 128-column block's
+ * largest), the last two under a power of two per 128 columns.  The down
+ * projection is one sum over the token's experts, rounded once to y, so results
+ * differ from moe_block_forward's in rounding only; they are reproducible bit
+ * for bit.  An infinity or a NaN in the weights of an expert reaches only the
+ * tokens routed to it; one in x or h, with E4M3 or 4-bit weights, its
+ * 128-column block of that token.  The second kernel needs every SM of the
+ * device: it starts when earlier work leaves them free.  ws:
+ * moe_decode_workspace_size() bytes, not shared with a call that may run at the
+ * same time.  T > 16 or F32 activations: MOE_ERR_UNSUPPORTED (use
+ * moe_block_forward). */
 MOE_API size_t moe_decode_workspace_size(const moe_problem* p);
 MOE_API moe_status moe_decode_forward(const moe_problem* p, const moe_block_options* opt, const void* x,
                              const void* w_router, const float* router_bias, const void* w_gate,

@@ -1892,7 +1892,7 @@ static DecodeLayout decode_layout(const moe_problem& p) {
     L.hsc = take(h_rows * (ldh_of(p) / 128) * 4);
   }
   L.gate = take((size_t)p.T * 4);
-  L.h = take(h_rows * ldh_of(p) * 2);
+  L.h = take(h_rows * ldh_of(p) * (p.w_dtype == MOE_BF16 ? 2 : 4));
   L.total = o;
   return L;
 }
@@ -2003,7 +2003,7 @@ extern "C" moe_status moe_decode_forward(const moe_problem* p, const moe_block_o
   a.hsc = (float*)(wsp + L.hsc);
   a.logits = (float*)(wsp + L.logits);
   a.splits = L.splits;
-  a.h = (bf16*)(wsp + L.h);
+  a.h = wsp + L.h;
   a.ldh = (int)ldh_of(*p);
   a.ids = topk_ids_out;
   a.tw = topk_w_out;

@@ -10,9 +10,9 @@
 //   1. every CTA adds the partials in slice order and selects each token's top k
 //      (one warp per token; the same code and inputs, so the same result in every
 //      CTA), and lists the active experts;
-//   2. gate/up: h[t, slot, f] = w * SiLU(W_g[f] x_t) * (W_u[f] x_t) in bf16, units of 16
+//   2. gate/up: h[t, slot, f] = w * SiLU(W_g[f] x_t) * (W_u[f] x_t), units of 16
 //      features of one expert.  The routing weight w is applied here, so that
-//   -- grid barrier (E4M3, mx4: h is prepared like x, and another barrier) --
+//   -- grid barrier (E4M3, mx4: h is scaled like x, and another barrier) --
 //   3. the down projection is ONE sum per output: y[t, n] = sum over the active
 //      experts and their features of W_d[n, f] h[t, slot, f], units of 16 outputs
 //      over all experts; fp32 throughout, rounded once, no atomics: reproducible.
@@ -77,7 +77,7 @@ struct DecodeArgs {
   float* xsc;           // [d / 128][kDecodeMaxT] its scales
   float* logits;        // [splits][T][E] partial logits
   int splits;
-  bf16* h;              // [T, k + 1, ldh]
+  void* h;              // [T, k + 1, ldh] bf16, or fp32 where h is scaled before the down projection
   uint8_t* hq;          // [T * (k + 1)][ldh / 32][64] h, scaled likewise
   float* hsc;           // [T * (k + 1)][ldh / 128] its scales
   int ldh;
@@ -782,7 +782,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a
         if (j < 0) continue;
         const float w = sh ? (a.gate ? __ldg(a.gate + t) : 1.f) : s.w[t][j];
         const float hv = w * (vg / (1.f + __expf(-vg)) * vu);
-        a.h[((int64_t)t * (a.k + 1) + j) * a.ldh + f] = __float2bfloat16_rn(hv);
+        const int64_t at = ((int64_t)t * (a.k + 1) + j) * a.ldh + f;
+        if (DecW<W>::SCALED) static_cast<float*>(a.h)[at] = hv;
+        else static_cast<bf16*>(a.h)[at] = __float2bfloat16_rn(hv);
       }
       if (kw > 1) team_sync(team, kw * 32);
       else __syncwarp();
@@ -861,9 +863,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a
       for (int i = blockIdx.x * kDecodeWarps + warp; i < n; i += gridDim.x * kDecodeWarps) {
         const int r = i / ldt, kb = i % ldt;
         if (kb * 128 >= (r % (a.k + 1) == a.k ? a.I_s : a.I)) continue;
-        const uint2 x = __ldcg(reinterpret_cast<const uint2*>(a.h + (int64_t)r * a.ldh + kb * 128 + lane * 4));
-        const float v[4] = {__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u), __uint_as_float(x.y << 16),
-                            __uint_as_float(x.y & 0xffff0000u)};
+        const float4 x =
+            __ldcg(reinterpret_cast<const float4*>(static_cast<const float*>(a.h) + (int64_t)r * a.ldh + kb * 128) + lane);
+        const float v[4] = {x.x, x.y, x.z, x.w};
         dec_split<W>(v, a.hq + (int64_t)i * 256, a.hsc + i, lane);
       }
       dec_grid_arrive(a.bar);

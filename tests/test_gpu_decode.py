@@ -7,12 +7,14 @@ bf16, relative):
   n * 2 * u32 times the sum of the products' magnitudes (the tensor core may
   truncate where a scalar addition rounds: one step, 2 * u32, each);
   h = w * silu(g) * u inherits g's and u's (|silu'| <= 1.1), the fast exponential
-  and the divisions (2^-18 together), the routing weight's own error, and one
-  rounding to bf16; y its sum's, plus one rounding to bf16.
+  and the divisions (2^-18 together), the routing weight's own error, and with
+  bf16 weights one rounding to bf16; y its sum's, plus one rounding to bf16.
 With E4M3 weights x and h enter their products as two E4M3 terms under one scale
 per 128 columns: off by at most half of the second term's smallest spacing, 2^-10,
-where the largest of the 128 is above 224; with 4-bit weights as f16 under such a
-scale: half of its smallest spacing, 2^-25, where the largest is at least 2^14.
+where the largest of the 128 is above 224, or 2^-8 relative (a term's half step,
+twice); with 4-bit weights as f16 under such a scale: half of its smallest
+spacing, 2^-25, where the largest is at least 2^14, or 2^-11 relative.  x, a
+bf16, is held exactly where that relative error is the larger.
 The routing weight: a logit's error moves a softmax weight by at most twice
 that, relatively; expf and the division add 2^-20."""
 import numpy as np
@@ -100,7 +102,7 @@ def _reference(kw, ref, gate=None, out=None):
         s = g * torch.sigmoid(g)
         h = wt * s * u
         dh = wt * (1.1 * dg * u.abs() + (s.abs() + 1.1 * dg) * du)
-        dh = dh + (h.abs() + dh) * (U16 + 2.0 ** -18 + wrel)
+        dh = dh + (h.abs() + dh) * ((2.0 ** -11 if p.w_dtype == 3 else U16) + 2.0 ** -18 + wrel)
         dh = dh + terms(h.abs() + dh)
         return wd @ h, wd.abs() @ dh, wd.abs() @ h.abs()
 
