@@ -28,7 +28,7 @@ BINDING_DEPS = [BINDING_SOURCE, os.path.join(ROOT, "include", "moe.h")]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
-    "-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
+    "-O3", "-lineinfo", "-std=c++20", "--expt-relaxed-constexpr",
     "-Xcompiler", "-fPIC,-O2,-fvisibility=hidden",
     "-shared", "-cudart", "static",
 ]

@@ -219,22 +219,20 @@ __device__ __forceinline__ bool has_edge_byte(uint32_t w) {
 }
 
 // acc[nb] += A * B over one piece.  bw[nb]: the lane's token data; xs[nb]: scales of
-// its two token columns.  A column block whose mask bit is clear is skipped.
+// its two token columns.
 template <int W, int NB>
 __device__ __forceinline__ void dec_mma(float (&acc)[NB][4], const DecFrag& f, const uint4 (&bw)[NB][DecW<W>::BV],
-                                        const float2 (&xs)[NB], unsigned nbmask) {
+                                        const float2 (&xs)[NB]) {
   if (W == kDecBf16) {
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-      if (nbmask >> nb & 1u) {
+    for (int nb = 0; nb < NB; ++nb) {
         mma_bf16(acc[nb], f.lo[0], f.hi[0], f.lo[1], f.hi[1], bw[nb][0].x, bw[nb][0].y);
         mma_bf16(acc[nb], f.lo[2], f.hi[2], f.lo[3], f.hi[3], bw[nb][0].z, bw[nb][0].w);
       }
   } else if (W == kDecFp8) {
     const float sc = __uint_as_float(f.s0);
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-      if (nbmask >> nb & 1u) {
+    for (int nb = 0; nb < NB; ++nb) {
         float p[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -274,8 +272,7 @@ __device__ __forceinline__ void dec_mma(float (&acc)[NB][4], const DecFrag& f, c
       mx4_to_f16(f.lo[b], l);
       mx4_to_f16(f.hi[b], h);
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-        if (nbmask >> nb & 1u) {
+      for (int nb = 0; nb < NB; ++nb) {
           const uint4 t = bw[nb][b % DecW<W>::BV];
           float p[4] = {0.f, 0.f, 0.f, 0.f};
           mma_f16(p, l[0], h[0], l[1], h[1], t.x, t.y);
@@ -288,9 +285,8 @@ __device__ __forceinline__ void dec_mma(float (&acc)[NB][4], const DecFrag& f, c
     }
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
-      if (nbmask >> nb & 1u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[nb][i] = fmaf(i & 1 ? xs[nb].y : xs[nb].x, sum[nb][i], acc[nb][i]);
+      for (int i = 0; i < 4; ++i) acc[nb][i] = fmaf(i & 1 ? xs[nb].y : xs[nb].x, sum[nb][i], acc[nb][i]);
   }
 }
 
@@ -382,6 +378,14 @@ __device__ __forceinline__ int team_warps(unsigned units, unsigned chunks, unsig
     key = min(cost, ~0u >> 3) << 3 | lane;  // (of equal costs the fewest warps)
   }
   return 1 << (__reduce_min_sync(0xffffffffu, key) & 7u);
+}
+
+// f<1>() or f<2>(): a block of columns is computed only where an expert has them (NB: the
+// most there can be), with registers for as many.
+template <int NB, typename F>
+__device__ __forceinline__ void dec_blocks(int cols, F f) {
+  if (NB == 1 || cols <= 8) f.template operator()<1>();
+  else f.template operator()<NB>();
 }
 
 __device__ __forceinline__ void team_sync(int team, int threads) {
@@ -727,54 +731,54 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a
       const int n0 = (sh ? u : (u - f_s) % f_r) * 16;
       const int N = sh ? a.I_s : a.I;
       const int cols = sh ? a.T : __popc(s.mask[ga]);  // tokens of the expert
-      const unsigned nbmask = cols > 8 ? 3u : 1u;
-      const uint8_t* tok[NB];
-      const float* tsc[NB];
+      dec_blocks<NB>(cols, [&]<int NU>() {
+        const uint8_t* tok[NU];
+        const float* tsc[NU];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        const int q = nb * 8 + g, t = sh || q >= cols ? q : s.col[ga][q] & 15;
-        tok[nb] = q < cols ? xin + t * xrow : nullptr;
-        tsc[nb] = a.xsc + t;
-      }
-      float ag[NB][4], au[NB][4];
+        for (int nb = 0; nb < NU; ++nb) {
+          const int q = nb * 8 + g, t = sh || q >= cols ? q : s.col[ga][q] & 15;
+          tok[nb] = q < cols ? xin + t * xrow : nullptr;
+          tsc[nb] = a.xsc + t;
+        }
+        float ag[NU][4], au[NU][4];
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+        for (int nb = 0; nb < NU; ++nb)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ag[nb][i] = au[nb][i] = 0.f;
-      for (int kc = tw; kc < nch_d; kc += kw) {
-        uint4 bw[NB][BV];
-        float2 xs[NB];
+          for (int i = 0; i < 4; ++i) ag[nb][i] = au[nb][i] = 0.f;
+        for (int kc = tw; kc < nch_d; kc += kw) {
+          uint4 bw[NU][BV];
+          float2 xs[NU];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-          if (nb == 0 || nbmask >> nb & 1u) {
+          for (int nb = 0; nb < NU; ++nb) {
             dec_tok<W>(bw[nb], tok[nb], kc, a.d, c);
             if (DecW<W>::SCALED) {  // lanes of group g hold column nb * 8 + g's; a lane wants columns 2c, 2c + 1
               const float v = tok[nb] ? __ldg(tsc[nb] + (kc * PC >> 7) * kDecodeMaxT) : 0.f;
               xs[nb] = make_float2(__shfl_sync(0xffffffffu, v, 8 * c), __shfl_sync(0xffffffffu, v, 8 * c + 4));
             }
           }
-        cp_async_wait<D - 1>();
-        __syncwarp();
-        DecFrag fg, fu;
-        const uint32_t at = ring + out_slot * kDecStage;
-        dec_read<W>(fg, at, at + 2 * kDecPiece, lane);
-        dec_read<W>(fu, at + kDecPiece, at + 2 * kDecPiece + kDecScales, lane);
-        out_slot = out_slot + 1 == D ? 0 : out_slot + 1;
-        __syncwarp();  // the stage has been read
-        issue();
-        dec_mma<W, NB>(ag, fg, bw, xs, nbmask);
-        dec_mma<W, NB>(au, fu, bw, xs, nbmask);
-      }
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          red[tw * RED + (nb * 4 + i) * 32 + lane] = ag[nb][i];
-          red[tw * RED + (NB * 4 + nb * 4 + i) * 32 + lane] = au[nb][i];
+          cp_async_wait<D - 1>();
+          __syncwarp();
+          DecFrag fg, fu;
+          const uint32_t at = ring + out_slot * kDecStage;
+          dec_read<W>(fg, at, at + 2 * kDecPiece, lane);
+          dec_read<W>(fu, at + kDecPiece, at + 2 * kDecPiece + kDecScales, lane);
+          out_slot = out_slot + 1 == D ? 0 : out_slot + 1;
+          __syncwarp();  // the stage has been read
+          issue();
+          dec_mma<W, NU>(ag, fg, bw, xs);
+          dec_mma<W, NU>(au, fu, bw, xs);
         }
+#pragma unroll
+        for (int nb = 0; nb < NU; ++nb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            red[tw * RED + (nb * 4 + i) * 32 + lane] = ag[nb][i];
+            red[tw * RED + (NB * 4 + nb * 4 + i) * 32 + lane] = au[nb][i];
+          }
+      });
       if (kw > 1) team_sync(team, kw * 32);
       else __syncwarp();
-      for (int q = tw * 32 + lane; q < NB * 128; q += kw * 32) {
+      for (int q = tw * 32 + lane; q < (cols > 8 ? NB : 1) * 128; q += kw * 32) {
         float vg = 0.f, vu = 0.f;
         for (int w = 0; w < kw; ++w) {
           vg += red[w * RED + q];
@@ -892,63 +896,63 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a
         const int K = sh ? a.I_s : a.I, nch = sh ? nch_s : nch_i;
         const int k1 = min(ks + left, sh ? nst_s : nst_i);
         const int cols = sh ? a.T : __popc(s.mask[ga]);  // tokens of the expert
-        const unsigned nbmask = cols > 8 ? 3u : 1u;
-        const uint8_t* tok[NB];
-        const float* tsc[NB];
+        dec_blocks<NB>(cols, [&]<int NU>() {
+          const uint8_t* tok[NU];
+          const float* tsc[NU];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          const int q = nb * 8 + g, v = q >= cols ? 0 : sh ? q | a.k << 4 : s.col[ga][q];
-          const int64_t r = (int64_t)(v & 15) * (a.k + 1) + (v >> 4);
-          tok[nb] = q < cols ? hin + r * hrow : nullptr;
-          tsc[nb] = a.hsc + r * ldt;
-        }
-        left -= k1 - ks;
-        // an expert's part reaches only its own tokens' sums, an infinity or a NaN in its
-        // weights too
-        float part[NB][4];
+          for (int nb = 0; nb < NU; ++nb) {
+            const int q = nb * 8 + g, v = q >= cols ? 0 : sh ? q | a.k << 4 : s.col[ga][q];
+            const int64_t r = (int64_t)(v & 15) * (a.k + 1) + (v >> 4);
+            tok[nb] = q < cols ? hin + r * hrow : nullptr;
+            tsc[nb] = a.hsc + r * ldt;
+          }
+          left -= k1 - ks;
+          // an expert's part reaches only its own tokens' sums, an infinity or a NaN in its
+          // weights too
+          float part[NU][4];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+          for (int nb = 0; nb < NU; ++nb)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) part[nb][r] = 0.f;
-        for (; ks < k1; ++ks) {
-          uint4 bw[2][NB][BV];
-          float2 xs[2][NB];
-          const bool two = 2 * ks + 1 < nch;
+            for (int r = 0; r < 4; ++r) part[nb][r] = 0.f;
+          for (; ks < k1; ++ks) {
+            uint4 bw[2][NU][BV];
+            float2 xs[2][NU];
+            const bool two = 2 * ks + 1 < nch;
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            if (nb > 0 && !(nbmask >> nb & 1u)) continue;
-            dec_tok<W>(bw[0][nb], tok[nb], 2 * ks, K, c);
-            dec_tok<W>(bw[1][nb], two ? tok[nb] : nullptr, 2 * ks + 1, K, c);
-            if (DecW<W>::SCALED) {
-              float v0 = 0.f, v1 = 0.f;
-              if (tok[nb]) {
-                v0 = tsc[nb][2 * ks * PC >> 7];
-                if (W == kDecMx4 && two) v1 = tsc[nb][2 * ks + 1];
+            for (int nb = 0; nb < NU; ++nb) {
+              dec_tok<W>(bw[0][nb], tok[nb], 2 * ks, K, c);
+              dec_tok<W>(bw[1][nb], two ? tok[nb] : nullptr, 2 * ks + 1, K, c);
+              if (DecW<W>::SCALED) {
+                float v0 = 0.f, v1 = 0.f;
+                if (tok[nb]) {
+                  v0 = tsc[nb][2 * ks * PC >> 7];
+                  if (W == kDecMx4 && two) v1 = tsc[nb][2 * ks + 1];
+                }
+                xs[0][nb] = make_float2(__shfl_sync(0xffffffffu, v0, 8 * c), __shfl_sync(0xffffffffu, v0, 8 * c + 4));
+                xs[1][nb] = W == kDecMx4 ? make_float2(__shfl_sync(0xffffffffu, v1, 8 * c), __shfl_sync(0xffffffffu, v1, 8 * c + 4))
+                                         : xs[0][nb];
               }
-              xs[0][nb] = make_float2(__shfl_sync(0xffffffffu, v0, 8 * c), __shfl_sync(0xffffffffu, v0, 8 * c + 4));
-              xs[1][nb] = W == kDecMx4 ? make_float2(__shfl_sync(0xffffffffu, v1, 8 * c), __shfl_sync(0xffffffffu, v1, 8 * c + 4))
-                                       : xs[0][nb];
             }
+            cp_async_wait<D - 1>();
+            __syncwarp();
+            DecFrag f0, f1;
+            const uint32_t at = ring + out_slot * kDecStage;
+            dec_read<W>(f0, at, at + 2 * kDecPiece, lane);
+            dec_read<W>(f1, at + kDecPiece, at + 2 * kDecPiece + kDecScales, lane);
+            out_slot = out_slot + 1 == D ? 0 : out_slot + 1;
+            __syncwarp();  // the stage has been read
+            issue();
+            dec_mma<W, NU>(part, f0, bw[0], xs[0]);
+            if (two) dec_mma<W, NU>(part, f1, bw[1], xs[1]);
           }
-          cp_async_wait<D - 1>();
-          __syncwarp();
-          DecFrag f0, f1;
-          const uint32_t at = ring + out_slot * kDecStage;
-          dec_read<W>(f0, at, at + 2 * kDecPiece, lane);
-          dec_read<W>(f1, at + kDecPiece, at + 2 * kDecPiece + kDecScales, lane);
-          out_slot = out_slot + 1 == D ? 0 : out_slot + 1;
-          __syncwarp();  // the stage has been read
-          issue();
-          dec_mma<W, NB>(part, f0, bw[0], xs[0], nbmask);
-          if (two) dec_mma<W, NB>(part, f1, bw[1], xs[1], nbmask);
-        }
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+          for (int nb = 0; nb < NU; ++nb)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int q = nb * 8 + 2 * c + (r & 1);
-            if (q < cols) sum[(sh ? q : s.col[ga][q] & 15) * 16 + g + (r >> 1) * 8] += part[nb][r];
-          }
+            for (int r = 0; r < 4; ++r) {
+              const int q = nb * 8 + 2 * c + (r & 1);
+              if (q < cols) sum[(sh ? q : s.col[ga][q] & 15) * 16 + g + (r >> 1) * 8] += part[nb][r];
+            }
+        });
         __syncwarp();  // (the next expert's columns are other lanes' tokens)
         ++ga;
         ks = 0;
