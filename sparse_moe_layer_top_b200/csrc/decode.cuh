@@ -733,12 +733,14 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a
       const int cols = sh ? a.T : __popc(s.mask[ga]);  // tokens of the expert
       dec_blocks<NB>(cols, [&]<int NU>() {
         const uint8_t* tok[NU];
-        const float* tsc[NU];
+        const float *sc0[NU], *sc1[NU];  // scales of the lane's product columns 2c, 2c + 1 of the block
+        auto token = [&](int q) { return sh || q >= cols ? q & 15 : s.col[ga][q] & 15; };
 #pragma unroll
         for (int nb = 0; nb < NU; ++nb) {
-          const int q = nb * 8 + g, t = sh || q >= cols ? q : s.col[ga][q] & 15;
-          tok[nb] = q < cols ? xin + t * xrow : nullptr;
-          tsc[nb] = a.xsc + t;
+          const int q = nb * 8 + g;
+          tok[nb] = q < cols ? xin + token(q) * xrow : nullptr;
+          sc0[nb] = a.xsc + token(nb * 8 + 2 * c);
+          sc1[nb] = a.xsc + token(nb * 8 + 2 * c + 1);
         }
         float ag[NU][4], au[NU][4];
 #pragma unroll
@@ -751,9 +753,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a
 #pragma unroll
           for (int nb = 0; nb < NU; ++nb) {
             dec_tok<W>(bw[nb], tok[nb], kc, a.d, c);
-            if (DecW<W>::SCALED) {  // lanes of group g hold column nb * 8 + g's; a lane wants columns 2c, 2c + 1
-              const float v = tok[nb] ? __ldg(tsc[nb] + (kc * PC >> 7) * kDecodeMaxT) : 0.f;
-              xs[nb] = make_float2(__shfl_sync(0xffffffffu, v, 8 * c), __shfl_sync(0xffffffffu, v, 8 * c + 4));
+            if (DecW<W>::SCALED) {
+              const int at = (kc * PC >> 7) * kDecodeMaxT;
+              xs[nb] = make_float2(__ldg(sc0[nb] + at), __ldg(sc1[nb] + at));
             }
           }
           cp_async_wait<D - 1>();
@@ -898,13 +900,17 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a
         const int cols = sh ? a.T : __popc(s.mask[ga]);  // tokens of the expert
         dec_blocks<NB>(cols, [&]<int NU>() {
           const uint8_t* tok[NU];
-          const float* tsc[NU];
+          const float *sc0[NU], *sc1[NU];  // scales of the lane's product columns 2c, 2c + 1 of the block
+          auto row = [&](int q) {  // of h; a column that does not exist: the first column's
+            const int v = sh ? (q < cols ? q : 0) | a.k << 4 : s.col[ga][q < cols ? q : 0];
+            return (v & 15) * (a.k + 1) + (v >> 4);
+          };
 #pragma unroll
           for (int nb = 0; nb < NU; ++nb) {
-            const int q = nb * 8 + g, v = q >= cols ? 0 : sh ? q | a.k << 4 : s.col[ga][q];
-            const int64_t r = (int64_t)(v & 15) * (a.k + 1) + (v >> 4);
-            tok[nb] = q < cols ? hin + r * hrow : nullptr;
-            tsc[nb] = a.hsc + r * ldt;
+            const int q = nb * 8 + g;
+            tok[nb] = q < cols ? hin + row(q) * hrow : nullptr;
+            sc0[nb] = a.hsc + row(nb * 8 + 2 * c) * ldt;
+            sc1[nb] = a.hsc + row(nb * 8 + 2 * c + 1) * ldt;
           }
           left -= k1 - ks;
           // an expert's part reaches only its own tokens' sums, an infinity or a NaN in its
@@ -923,14 +929,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a
               dec_tok<W>(bw[0][nb], tok[nb], 2 * ks, K, c);
               dec_tok<W>(bw[1][nb], two ? tok[nb] : nullptr, 2 * ks + 1, K, c);
               if (DecW<W>::SCALED) {
-                float v0 = 0.f, v1 = 0.f;
-                if (tok[nb]) {
-                  v0 = tsc[nb][2 * ks * PC >> 7];
-                  if (W == kDecMx4 && two) v1 = tsc[nb][2 * ks + 1];
-                }
-                xs[0][nb] = make_float2(__shfl_sync(0xffffffffu, v0, 8 * c), __shfl_sync(0xffffffffu, v0, 8 * c + 4));
-                xs[1][nb] = W == kDecMx4 ? make_float2(__shfl_sync(0xffffffffu, v1, 8 * c), __shfl_sync(0xffffffffu, v1, 8 * c + 4))
-                                         : xs[0][nb];
+                const int kb = 2 * ks * PC >> 7;  // (E4M3: both pieces are in it)
+                xs[0][nb] = xs[1][nb] = make_float2(sc0[nb][kb], sc1[nb][kb]);
+                if (W == kDecMx4 && two) xs[1][nb] = make_float2(sc0[nb][kb + 1], sc1[nb][kb + 1]);
               }
             }
             cp_async_wait<D - 1>();
