@@ -122,12 +122,26 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_e4m3_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {  // d = A * B
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {  // d = A * B
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 // Four 8x8 tiles of 16-bit elements, one row address a lane: word c of row g of each.
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t at) {
@@ -233,11 +247,12 @@ __device__ __forceinline__ void dec_mma(float (&acc)[NB][4], const DecFrag& f, c
     const float sc = __uint_as_float(f.s0);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-        float p[4] = {0.f, 0.f, 0.f, 0.f};
+        float p[4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const uint4 b = bw[nb][i % DecW<W>::BV];
-          mma_e4m3(p, f.lo[2 * i], f.hi[2 * i], f.lo[2 * i + 1], f.hi[2 * i + 1], b.x, b.y);
+          if (i == 0) mma_e4m3_first(p, f.lo[0], f.hi[0], f.lo[1], f.hi[1], b.x, b.y);
+          else mma_e4m3(p, f.lo[2 * i], f.hi[2 * i], f.lo[2 * i + 1], f.hi[2 * i + 1], b.x, b.y);
           mma_e4m3(p, f.lo[2 * i], f.hi[2 * i], f.lo[2 * i + 1], f.hi[2 * i + 1], b.z, b.w);
         }
         const float s0 = sc * xs[nb].x, s1 = sc * xs[nb].y;
@@ -274,8 +289,8 @@ __device__ __forceinline__ void dec_mma(float (&acc)[NB][4], const DecFrag& f, c
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
           const uint4 t = bw[nb][b % DecW<W>::BV];
-          float p[4] = {0.f, 0.f, 0.f, 0.f};
-          mma_f16(p, l[0], h[0], l[1], h[1], t.x, t.y);
+          float p[4];
+          mma_f16_first(p, l[0], h[0], l[1], h[1], t.x, t.y);
           mma_f16(p, l[2], h[2], l[3], h[3], t.z, t.w);
           sum[nb][0] = fmaf(s0[b], p[0], sum[nb][0]);
           sum[nb][1] = fmaf(s0[b], p[1], sum[nb][1]);
@@ -290,15 +305,16 @@ __device__ __forceinline__ void dec_mma(float (&acc)[NB][4], const DecFrag& f, c
   }
 }
 
-// Token data of piece kc for the lane's token column (p: its row, NULL: zeros).
+// Token data of piece kc for the lane's token column (p: its row).
 template <int W>
 __device__ __forceinline__ void dec_tok(uint4 (&bw)[DecW<W>::BV], const uint8_t* p, int kc, int K, int c) {
-  // bf16: 8 columns a lane; terms: 16 bytes a lane and 32-column block
-  const bool ok = p && (W != kDecBf16 || kc * 32 + c * 8 < K);
+  // bf16: 8 columns a lane, zeros past the last (they meet the weights' zeros); scaled:
+  // 16 bytes a lane and 32-column block
 #pragma unroll
   for (int i = 0; i < DecW<W>::BV; ++i) {
-    bw[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (ok) bw[i] = *reinterpret_cast<const uint4*>(p + ((int64_t)kc * DecW<W>::BV + i) * 64 + c * 16);
+    const uint4* q = reinterpret_cast<const uint4*>(p + (kc * DecW<W>::BV + i) * 64 + c * 16);
+    if (W != kDecBf16 || kc * 32 + c * 8 < K) bw[i] = *q;
+    else bw[i] = make_uint4(0u, 0u, 0u, 0u);
   }
 }
 
@@ -734,11 +750,12 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a
       dec_blocks<NB>(cols, [&]<int NU>() {
         const uint8_t* tok[NU];
         const float *sc0[NU], *sc1[NU];  // scales of the lane's product columns 2c, 2c + 1 of the block
-        auto token = [&](int q) { return sh || q >= cols ? q & 15 : s.col[ga][q] & 15; };
+        // of column q; of one that does not exist the first's (the product's column is not used)
+        auto token = [&](int q) { return sh ? (q < cols ? q : 0) : s.col[ga][q < cols ? q : 0] & 15; };
 #pragma unroll
         for (int nb = 0; nb < NU; ++nb) {
           const int q = nb * 8 + g;
-          tok[nb] = q < cols ? xin + token(q) * xrow : nullptr;
+          tok[nb] = xin + token(q) * xrow;
           sc0[nb] = a.xsc + token(nb * 8 + 2 * c);
           sc1[nb] = a.xsc + token(nb * 8 + 2 * c + 1);
         }
@@ -908,7 +925,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a
 #pragma unroll
           for (int nb = 0; nb < NU; ++nb) {
             const int q = nb * 8 + g;
-            tok[nb] = q < cols ? hin + row(q) * hrow : nullptr;
+            tok[nb] = hin + row(q) * hrow;
             sc0[nb] = a.hsc + row(nb * 8 + 2 * c) * ldt;
             sc1[nb] = a.hsc + row(nb * 8 + 2 * c + 1) * ldt;
           }
@@ -927,7 +944,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a
 #pragma unroll
             for (int nb = 0; nb < NU; ++nb) {
               dec_tok<W>(bw[0][nb], tok[nb], 2 * ks, K, c);
-              dec_tok<W>(bw[1][nb], two ? tok[nb] : nullptr, 2 * ks + 1, K, c);
+              dec_tok<W>(bw[1][nb], tok[nb], two ? 2 * ks + 1 : 2 * ks, K, c);
               if (DecW<W>::SCALED) {
                 const int kb = 2 * ks * PC >> 7;  // (E4M3: both pieces are in it)
                 xs[0][nb] = xs[1][nb] = make_float2(sc0[nb][kb], sc1[nb][kb]);
