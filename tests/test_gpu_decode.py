@@ -337,3 +337,29 @@ def test_layer_object_quantise_and_decode_together():
         assert (got.float() - y[lo:hi].float()).norm() <= 1e-2 * y[lo:hi].float().norm()
     with pytest.raises(moe.MoEError, match="moe_layer_forward"):
         layer.decode(inp.x[:17])
+
+
+@pytest.mark.parametrize("w,T", [("fp8", 6), ("mx4", 6), ("fp8", 12), ("mx4", 12)])
+def test_infinite_and_nan_tokens_stay_their_own_with_scaled_weights(w, T):
+    kw, _ = _make(T, 256, 16, 3, 128, 128, w, seed=13)
+    y0, ids0, _ = _run(kw)
+    kw["x"][2, 11] = float("nan")
+    kw["x"][5, 100] = float("inf")
+    y, ids, _ = _run(kw)
+    keep = [t for t in range(T) if t not in (2, 5)]
+    assert torch.equal(y[keep], y0[keep]) and torch.equal(ids[keep], ids0[keep])
+    assert torch.isnan(y[2]).all() and not torch.isfinite(y[5]).any()
+
+
+@pytest.mark.parametrize("w", ["bf16", "fp8", "mx4"])
+@pytest.mark.parametrize("T", [8, 9, 16])
+def test_every_token_at_one_expert(w, T):
+    """The bias sends all tokens to the same experts: full column blocks, and a
+    second one from nine tokens on."""
+    E, k = 20, 2
+    bias = torch.full((E,), -50.0)
+    bias[[3, 17]] = 50.0
+    kw, ref = _make(T, 384, E, k, 256, 0, w, seed=14 + T, bias=bias)
+    out = _run(kw)
+    assert (out[1].cpu().sort(1).values == torch.tensor([3, 17])).all()
+    _check(out, _reference(kw, ref, out=out))
