@@ -111,7 +111,9 @@ __device__ __forceinline__ float mx_split_inv(uint32_t b) {  // a NaN block mult
 // One block of 256 threads per 128 x 128 tile: 16 threads a row, 8 values a
 // thread, 4 threads a scale block (two shuffles), 8 row passes whose loads are
 // all issued before the first is used.  Memory bound: 2 (4) bytes read and 17/32
-// written per value.
+// written per value.  256 x 2048 x 512 bf16 values quantised and read back 260 us
+// (207 at the copy rate); with 128, 512, 1024 threads a tile 287, 258, 337 us, 2048 x
+// 8192 values 22.8 us (26.7, 24.6, 26.8); a block per two tiles, a warp a row, 288.
 template <typename TA>
 __device__ __forceinline__ void load8(const TA* p, float (&v)[8]);
 template <>

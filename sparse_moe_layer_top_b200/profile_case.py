@@ -6,7 +6,8 @@ benchmark workloads:
     python -m sparse_moe_layer_top_b200.profile_case --T 64 --d 8192 --E 32 --k 10 --I 2048 --w bf16
     python -m sparse_moe_layer_top_b200.profile_case --config qwen38max_prefill_zipf_bf16 --reps 3
 
-(--config runs a named benchmark workload at its full size instead.)
+(--config runs a named benchmark workload at its full size instead; --w mx4
+quantises bf16 weights on the GPU; --decode runs the few-token form.)
 
 Inputs come from moe_inputs (seeded).  Exits non-zero if the device status
 word reports a fault.
@@ -24,9 +25,10 @@ def arg_parser():
     ap.add_argument("--k", type=int, default=10)
     ap.add_argument("--I", type=int, default=2048)
     ap.add_argument("--Is", type=int, default=2048)
-    ap.add_argument("--w", choices=("bf16", "fp8"), default="bf16")
+    ap.add_argument("--w", choices=("bf16", "fp8", "mx4"), default="bf16")
     ap.add_argument("--bias", choices=("none", "zipf"), default="none")
     ap.add_argument("--path", type=int, default=0)
+    ap.add_argument("--decode", action="store_true", help="the few-token form (T at most 16)")
     ap.add_argument("--reps", type=int, default=2)
     ap.add_argument("--config", default=None, help="a named workload of moe_inputs.CONFIGS, at its full size")
     return ap
@@ -46,12 +48,17 @@ def main(argv=None):
     if a.config:
         inp = moe_inputs.make_config(a.config, seed=0, device="cuda")
     else:
-        inp = moe_inputs.make_inputs(a.T, a.d, a.E, a.k, a.I, a.Is, act="bf16", w=a.w,
+        inp = moe_inputs.make_inputs(a.T, a.d, a.E, a.k, a.I, a.Is, act="bf16", w="bf16" if a.w == "mx4" else a.w,
                                      bias=None if a.bias == "none" else a.bias, seed=0, device="cuda")
     moe.set_path(a.path)
-    layer = moe.MoELayer.from_inputs(inp, max_tokens=inp.T)
+    if a.w == "mx4" and not a.config:
+        *codes, scales = moe.quantize_experts_mx4(inp.wg, inp.wu, inp.wd, inp.s_wg, inp.s_wu, inp.s_wd)
+        layer = moe.MoELayer(inp.d, inp.E, inp.k, inp.I, inp.I_s, inp.w_r, *codes, bias=inp.bias, scales=scales, w="mx4",
+                             max_tokens=inp.T)
+    else:
+        layer = moe.MoELayer.from_inputs(inp, max_tokens=inp.T)
     for _ in range(a.reps):
-        y = layer(inp.x)
+        y = layer.decode(inp.x) if a.decode else layer(inp.x)
     torch.cuda.synchronize()
     status, detail = moe.device_status()
     if status != 0:
