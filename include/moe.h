@@ -301,8 +301,8 @@ MOE_API moe_status moe_router_topk_static(const moe_problem* p, const void* x, c
  * expert_form: 0 SIMT kernels, 1 row-tiled tensor-core GEMMs, 2 weight-row
  * (swap-AB) GEMMs, 3 row-tiled GEMMs on CTA pairs, 4 split (CTA pairs for the
  * groups of 256 rows or more, weight-row GEMMs for the others), 5 GEMMs on CTA
- * pairs with the tokens as the MMA's N, 6 weight-row GEMMs on 4-bit weights
- * (block-scaled tensor cores, bf16 rows split into two E4M3 planes);
+ * pairs with the tokens as the MMA's N, 6 GEMMs on 4-bit weights (block-scaled
+ * tensor cores, a bf16 row entering as two E4M3 rows);
  * router_selects: 1 when the
  * router's GEMM selects the top k in its epilogue (bf16, E <= 256, at least
  * 16 tiles of 128 tokens), 0 for the split-K GEMM + top-k kernel or the SIMT

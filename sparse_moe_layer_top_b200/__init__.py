@@ -511,7 +511,7 @@ def rmsnorm(prob, x, norm_weight, eps=1e-6, out=None, stream=None):
     return out
 
 
-EXPERT_FORMS = ("simt", "rows", "weight_rows", "cta_pairs", "split", "cta_pairs_tokens_n", "weight_rows_mx4")
+EXPERT_FORMS = ("simt", "rows", "weight_rows", "cta_pairs", "split", "cta_pairs_tokens_n", "mx4")
 
 
 def forward_plan(prob):

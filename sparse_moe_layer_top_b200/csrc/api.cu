@@ -509,7 +509,7 @@ static moe_status choose_form(const moe_problem& p, int* form) {
   moe_status s = choose(tc_shapes(p), &tc);
   if (s != MOE_OK) return s;
   if (!tc) *form = kFormSimt;
-  else if (p.w_dtype == MOE_MXFP4_B32) *form = kFormMx4;  // one form: weight rows as M, 64-token chunks as N
+  else if (p.w_dtype == MOE_MXFP4_B32) *form = kFormMx4;  // one form for every group size
   else if (g_path == 2) *form = kFormRows;
   else if (g_path == 3) *form = kFormSwap;
   else if (g_path == 4) *form = p.w_dtype == MOE_BF16 ? kFormPair : kFormRows;
@@ -1417,7 +1417,7 @@ static void schedules(const moe_problem& p, int form, Schedule* sa, Schedule* sb
   } else if (form == kFormSwap) {  // (token chunk, 128 weight rows) tiles; E4M3 down: 256 rows
     *sa = Schedule{kNCH, 128, p.I, p.I_s, 0, 0, 0, 0};
     *sb = Schedule{kNCH, p.w_dtype == MOE_FP8_E4M3_B128 ? 256 : 128, p.d, p.d, 0, 0, 0, 0};
-  } else if (form == kFormMx4) {  // (token chunk, 128 features of gate and up / 256 outputs) tiles
+  } else if (form == kFormMx4) {  // (64-token chunk, 128 features of gate and up / 256 outputs) tiles
     *sa = Schedule{kNCH, 128, p.I, p.I_s, 0, 0, 0, 0};
     *sb = Schedule{kNCH, 256, p.d, p.d, 0, 0, 0, 0};
   } else if (form == kFormSplit) {  // pair tiles for the large groups, weight-row tiles for the rest

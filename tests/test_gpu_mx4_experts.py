@@ -6,8 +6,8 @@ Error bound of an element (u32 = 2^-24, u16 = 2^-8, half a step relative):
   2^-21 of the largest value of its 32 (half a step of the second term's
   smallest spacing, 2^-9 / 16, against a largest value above 224);
   a sum of n products: n * 2 * u32 of the products' magnitudes;
-  the activation h is rounded to bf16 once (and its exponential and division
-  are good to 2^-18), the result once."""
+  the activation h is rounded once, to bf16 or to two such terms (2^-4 twice;
+  its exponential and division are good to 2^-18), the result once."""
 import numpy as np
 import pytest
 import torch
@@ -199,7 +199,7 @@ def test_forward_matches_oracle(case, path):
     if differ:
         y_or, *_ = oracle.moe_forward(*args, bias=inp.bias, force_ids=use)
     assert rel_l2(y.float().cpu().numpy(), y_or) <= 1e-2
-    assert moe.forward_plan(prob)["expert_form"] == ("simt" if path == 1 else "weight_rows_mx4")
+    assert moe.forward_plan(prob)["expert_form"] == ("simt" if path == 1 else "mx4")
 
 
 def test_forward_with_norm_gate_and_replay():
@@ -283,3 +283,27 @@ def test_misaligned_weights_are_refused():
     offs = torch.tensor([0, 4, 4, 4], dtype=torch.int32, device="cuda")
     with pytest.raises(moe.MoEError, match="32-byte"):
         moe.expert_ffn(prob, x, offs, w, good.view(E, I, d // 2), good, scales=scales)
+
+
+def test_waits_that_run_out_report_timeout_and_the_device_stays_usable():
+    """The bound set far below the kernel's longer waits: the call comes back, the
+    status names the kernel, and the same call then gives the same bits."""
+    T, d, E, I = 200, 8192, 4, 256
+    g = torch.Generator(device="cuda").manual_seed(15)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda", dtype=torch.float32) * 0.05
+    *codes, scales = moe.quantize_experts_mx4(r(E, I, d), r(E, I, d), r(E, d, I))
+    offs = torch.tensor([0, 60, 70, 70, T, T], dtype=torch.int32, device="cuda")
+    x = r(T, d).to(torch.bfloat16)
+    prob = moe.Problem.make(T, d, E, 1, I, 0, "bf16", "mx4")
+    want = moe.expert_ffn(prob, x, offs, *codes, scales=scales)
+    torch.cuda.synchronize()
+    assert moe.device_status()[0] == 0
+    moe.set_wait_limit(100)
+    try:
+        moe.expert_ffn(prob, x, offs, *codes, scales=scales)
+        s, detail = moe.device_status()
+        assert s == 7 and (detail >> 8) & 0xff == 5 and 1 <= detail & 0xff <= 6, (s, hex(detail))
+    finally:
+        moe.set_wait_limit(0)
+    y = moe.expert_ffn(prob, x, offs, *codes, scales=scales)
+    assert moe.device_status()[0] == 0 and torch.equal(y, want)
