@@ -446,21 +446,31 @@ __device__ __forceinline__ void dec_topk(const float* logits, int E, int k, int 
     if (l[i] != l[i]) q = 1u;
     key[i] = e < E ? q : 0u;
   }
+  // the lane's best and its lowest holder; only the lane that loses it looks again
+  uint32_t best;
+  unsigned at;
+  auto look = [&]() {
+    best = key[0];
+    at = lane;
+#pragma unroll
+    for (int i = 1; i < NPL; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        at = lane + 32 * i;
+      }
+  };
+  look();
   unsigned my_e = 0;
   for (int j = 0; j < k; ++j) {
-    uint32_t best = 0;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) best = max(best, key[i]);
     const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-    unsigned cand = 0xffffffffu;
-#pragma unroll
-    for (int i = NPL - 1; i >= 0; --i)
-      if (key[i] == top && lane + 32 * i < E) cand = lane + 32 * i;
-    const unsigned e = __reduce_min_sync(0xffffffffu, cand);
-#pragma unroll
-    for (int i = 0; i < NPL; ++i)
-      if (e == (unsigned)(lane + 32 * i)) key[i] = 0u;
+    const unsigned e = __reduce_min_sync(0xffffffffu, best == top && at < (unsigned)E ? at : 0xffffffffu);
     if (lane == j) my_e = e;
+    if (e == at) {
+#pragma unroll
+      for (int i = 0; i < NPL; ++i)
+        if (e == (unsigned)(lane + 32 * i)) key[i] = 0u;
+      look();
+    }
   }
   const float mine = lane < k ? logits[my_e] : 0.f, top = __shfl_sync(0xffffffffu, mine, 0);
   const float p = lane < k ? expf(mine - top) : 0.f;
@@ -634,8 +644,14 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a
     const int n = a.T * a.E;
     for (int i = tid; i < n; i += kDecodeThreads) {
       float v = a.bias ? __ldg(a.bias + i % a.E) : 0.f;
-#pragma unroll 4
-      for (int p = 0; p < a.splits; ++p) v += __ldcg(a.logits + (int64_t)p * n + i);
+      for (int p0 = 0; p0 < a.splits; p0 += 8) {  // eight in flight, added in order
+        float part[8];
+#pragma unroll
+        for (int p = 0; p < 8; ++p) part[p] = p0 + p < a.splits ? __ldcg(a.logits + (p0 + p) * n + i) : 0.f;
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+          if (p0 + p < a.splits) v += part[p];
+      }
       lg[i] = v;
     }
     s.flag[tid] = 0;
