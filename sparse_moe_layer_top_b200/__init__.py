@@ -10,7 +10,9 @@ types and sizes against the problem and raises ValueError, before any pointer
 is taken, when a buffer is of the wrong type or too small for what the call
 reads or writes.  The library launches on the current CUDA device and its
 current stream: every call also requires all its tensors (and a stream it is
-given) to be on one device, and runs with that device current.
+given) to be on one device, and runs with that device current.  What a call
+allocates (outputs that were not given, a workspace) belongs to the stream the
+call runs on; a caller that uses an output on another stream orders the two.
 
 Entry points mirror ``include/moe.h``: ``router_topk``, ``permute``,
 ``expert_ffn``, ``combine``, ``layer_forward``, ``block_forward``,
@@ -351,12 +353,12 @@ def router_topk(prob, x, w_router, bias=None, topk_ids=None, topk_w=None, ws=Non
     _need(topk_ids, "topk_ids", T * k, _I32, k)
     _need(topk_w, "topk_w", T * k, _F32, k)
     dev = _device(stream, x=x, w_router=w_router, router_bias=bias, topk_ids=topk_ids, topk_w=topk_w, ws=ws)
-    if topk_ids is None:
-        topk_ids = torch.empty((T, k), dtype=torch.int32, device=x.device)
-    if topk_w is None:
-        topk_w = torch.empty((T, k), dtype=torch.float32, device=x.device)
-    ws = _ws(stage_workspace_size(prob), x.device, ws)
-    with _current(dev):
+    with _current(dev), _alloc(stream):
+        if topk_ids is None:
+            topk_ids = torch.empty((T, k), dtype=torch.int32, device=x.device)
+        if topk_w is None:
+            topk_w = torch.empty((T, k), dtype=torch.float32, device=x.device)
+        ws = _ws(stage_workspace_size(prob), x.device, ws)
         _check(lib().moe_router_topk(ctypes.byref(prob), _ptr(x), _ptr(w_router), _ptr(bias), _ptr(topk_ids),
                                      _ptr(topk_w), _ptr(ws), _nbytes(ws), _stream(stream)))
     return topk_ids, topk_w
@@ -374,14 +376,13 @@ def permute(prob, x, topk_ids, topk_w, ws=None, stream=None):
     cur = _device(stream, x=x, topk_ids=topk_ids, topk_w=topk_w, ws=ws)
     dev = x.device
     Rp = rows_total(prob)
-    out = dict(x_perm=torch.empty((Rp, prob.d), dtype=_act(prob), device=dev),
-               row_tok=torch.empty(Rp, dtype=torch.int32, device=dev),
-               row_w=torch.empty(Rp, dtype=torch.float32, device=dev),
-               pos=torch.empty((prob.T, prob.k), dtype=torch.int32, device=dev),
-               offs=torch.empty(prob.E + 2, dtype=torch.int32, device=dev))
-    nbytes = stage_workspace_size(prob)
-    ws = _ws(nbytes, dev, ws)
-    with _current(cur):
+    with _current(cur), _alloc(stream):
+        out = dict(x_perm=torch.empty((Rp, prob.d), dtype=_act(prob), device=dev),
+                   row_tok=torch.empty(Rp, dtype=torch.int32, device=dev),
+                   row_w=torch.empty(Rp, dtype=torch.float32, device=dev),
+                   pos=torch.empty((prob.T, prob.k), dtype=torch.int32, device=dev),
+                   offs=torch.empty(prob.E + 2, dtype=torch.int32, device=dev))
+        ws = _ws(stage_workspace_size(prob), dev, ws)
         _check(lib().moe_permute(ctypes.byref(prob), _ptr(x), _ptr(topk_ids), _ptr(topk_w), _ptr(out["x_perm"]),
                                  _ptr(out["row_tok"]), _ptr(out["row_w"]), _ptr(out["pos"]), _ptr(out["offs"]),
                                  _ptr(ws), _nbytes(ws), _stream(stream)))
@@ -402,10 +403,10 @@ def expert_ffn(prob, x_perm, offs, wg, wu, wd, s_wg=None, s_wu=None, s_wd=None, 
     cur = _device(stream, x_perm=x_perm, offs=offs, w_gate=wg, w_up=wu, w_down=wd, ws_gate=s_wg, ws_up=s_wu,
                   ws_down=s_wd, scales=scales, y_perm=y_perm, ws=ws)
     dev = x_perm.device
-    if y_perm is None:
-        y_perm = torch.empty((x_perm.shape[0], prob.d), dtype=_act(prob), device=dev)
-    ws = _ws(stage_workspace_size(prob), dev, ws)
-    with _current(cur):
+    with _current(cur), _alloc(stream):
+        if y_perm is None:
+            y_perm = torch.empty((x_perm.shape[0], prob.d), dtype=_act(prob), device=dev)
+        ws = _ws(stage_workspace_size(prob), dev, ws)
         _check(lib().moe_expert_ffn(ctypes.byref(prob), _ptr(x_perm), _ptr(offs), _ptr(wg), _ptr(wu), _ptr(wd),
                                     _ptr(s_wg), _ptr(s_wu), _ptr(s_wd), _ptr(scales), _ptr(y_perm), _ptr(ws),
                                     _nbytes(ws), _stream(stream)))
@@ -420,9 +421,9 @@ def combine(prob, y_perm, pos, topk_w, offs, y=None, stream=None):
     _need(offs, "offs", prob.E + 2, _I32)
     _need(y, "y", prob.T * prob.d, a, prob.d)
     cur = _device(stream, y_perm=y_perm, pos=pos, topk_w=topk_w, offs=offs, y=y)
-    if y is None:
-        y = torch.empty((prob.T, prob.d), dtype=_act(prob), device=y_perm.device)
-    with _current(cur):
+    with _current(cur), _alloc(stream):
+        if y is None:
+            y = torch.empty((prob.T, prob.d), dtype=_act(prob), device=y_perm.device)
         _check(lib().moe_combine(ctypes.byref(prob), _ptr(y_perm), _ptr(pos), _ptr(topk_w), _ptr(offs), _ptr(y),
                                  _stream(stream)))
     return y
@@ -454,10 +455,10 @@ def _forward(prob, x, w_router, bias, wg, wu, wd, s_wg, s_wu, s_wd, scales, norm
     cur = _device(stream, x=x, w_router=w_router, router_bias=bias, w_gate=wg, w_up=wu, w_down=wd, ws_gate=s_wg,
                   ws_up=s_wu, ws_down=s_wd, scales=scales, norm_weight=norm_weight, shared_gate=shared_gate, y=y,
                   topk_ids=topk_ids, topk_w=topk_w, ws=ws)
-    if y is None:
-        y = torch.empty((prob.T, prob.d), dtype=_act(prob), device=x.device)
-    ws = _ws(workspace_size(prob), x.device, ws)
-    with _current(cur):
+    with _current(cur), _alloc(stream):
+        if y is None:
+            y = torch.empty((prob.T, prob.d), dtype=_act(prob), device=x.device)
+        ws = _ws(workspace_size(prob), x.device, ws)
         _forward_call(prob, x, w_router, bias, wg, wu, wd, s_wg, s_wu, s_wd, scales, norm_weight, norm_eps,
                       shared_gate, y, topk_ids, topk_w, ws, stream, block)
     return y
@@ -503,9 +504,9 @@ def rmsnorm(prob, x, norm_weight, eps=1e-6, out=None, stream=None):
     _need(norm_weight, "norm_weight", prob.d, a)
     _need(out, "out", prob.T * prob.d, a, prob.d)
     cur = _device(stream, x=x, norm_weight=norm_weight, out=out)
-    if out is None:
-        out = torch.empty_like(x)
-    with _current(cur):
+    with _current(cur), _alloc(stream):
+        if out is None:
+            out = torch.empty_like(x)
         _check(lib().moe_rmsnorm(ctypes.byref(prob), _ptr(x), _ptr(norm_weight), float(eps), _ptr(out),
                                  _stream(stream)))
     return out
@@ -529,9 +530,9 @@ def ep_expand_ids(counts, G, E_local, R, ids=None, stream=None):
     _need(counts, "counts", int(G) * int(E_local), _I32)
     _need(ids, "ids", int(R), _I32)
     cur = _device(stream, counts=counts, ids=ids)
-    if ids is None:
-        ids = torch.empty(max(int(R), 0), dtype=torch.int32, device=counts.device)
-    with _current(cur):
+    with _current(cur), _alloc(stream):
+        if ids is None:
+            ids = torch.empty(max(int(R), 0), dtype=torch.int32, device=counts.device)
         _check(lib().moe_ep_expand_ids(_ptr(counts), int(G), int(E_local), int(R), _ptr(ids), _stream(stream)))
     return ids
 

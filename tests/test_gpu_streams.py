@@ -1,0 +1,53 @@
+"""Calls on a stream that is not torch's current one: nothing that the current
+stream allocates and writes while they run reaches their workspace or outputs."""
+import pytest
+import torch
+
+import moe_inputs
+import sparse_moe_layer_top_b200 as moe
+
+pytestmark = pytest.mark.gpu
+
+T, D, E, K, I, I_S = 200, 1024, 16, 4, 512, 256
+
+
+def _inputs(w, T=T):
+    inp = moe_inputs.make_inputs(T, D, E, K, I, I_S, seed=21, device="cuda")
+    W, scales = [inp.wg, inp.wu, inp.wd, inp.s_wg, inp.s_wu, inp.s_wd], None
+    if w == "mx4":
+        *W, scales = moe.quantize_experts_mx4(*W)
+    return inp, W, scales
+
+
+def _overwrite(nbytes):
+    """What a program does next on the current stream: buffers of a workspace's
+    and of an output's size, written at once."""
+    for n in (nbytes, nbytes // 2, 2 * T * (K + 1) * D, 2 * T * D):
+        torch.empty(max(n, 1), dtype=torch.uint8, device="cuda").fill_(255)
+
+
+@pytest.mark.parametrize("w", ["bf16", "mx4"])
+def test_calls_without_a_workspace_on_a_side_stream(w):
+    inp, W, scales = _inputs(w)
+    prob = moe.Problem.make(T, D, E, K, I, I_S, "bf16", w)
+    few = moe.Problem.make(9, D, E, K, I, I_S, "bf16", w)
+    ids, tw = moe.router_topk(prob, inp.x, inp.w_r)
+    perm = moe.permute(prob, inp.x, ids, tw)
+    s = torch.cuda.Stream()
+    calls = [
+        (lambda **kw: moe.expert_ffn(prob, perm["x_perm"], perm["offs"], *W, scales=scales, **kw),
+         moe.stage_workspace_size(prob)),
+        (lambda **kw: moe.layer_forward(prob, inp.x, inp.w_r, None, *W, scales=scales, **kw),
+         moe.workspace_size(prob)),
+        (lambda **kw: moe.decode_forward(few, inp.x[:9], inp.w_r, None, *W, scales=scales, **kw),
+         moe.decode_workspace_size(few)),
+    ]
+    for call, nbytes in calls:
+        want = call()
+        torch.cuda.synchronize()
+        for _ in range(5):
+            got = call(stream=s)
+            _overwrite(nbytes)
+            torch.cuda.synchronize()
+            assert torch.equal(got, want)
+    assert moe.device_status()[0] == 0

@@ -1,0 +1,96 @@
+"""What the binding allocates for a call belongs to the stream the call runs on.
+
+The caching allocator hands a freed block out again on the stream that it was
+allocated on, at once: a workspace from another stream's pool may still be used
+by work queued there, and goes back there while the call's own kernels run.
+Here, without a GPU, torch.cuda.stream and the library's launches are replaced
+by recorders; the calls themselves are the binding's."""
+import contextlib
+
+import pytest
+import torch
+
+import sparse_moe_layer_top_b200 as moe
+
+T, D, E, K, I = 12, 128, 4, 2, 128
+ROWS = T * (K + 1)
+
+
+class Stream:
+    def __init__(self, handle):
+        self.cuda_stream = handle
+        self.device = torch.device("cpu")
+
+
+@pytest.fixture
+def recorded(monkeypatch):
+    """-> (list of the stream in effect at each allocation, list of (entry point, stream) launches)."""
+    allocs, launches, stack = [], [], []
+
+    @contextlib.contextmanager
+    def use(stream):
+        stack.append(stream)
+        try:
+            yield
+        finally:
+            stack.pop()
+
+    class Lib:
+        def __getattr__(self, name):
+            if name.endswith("_size") or name.endswith("_bytes"):
+                return getattr(real, name)
+            return lambda *a: launches.append((name, a[-1])) or 0
+
+    real, empty, empty_like = moe.lib(), torch.empty, torch.empty_like
+    monkeypatch.setattr(moe, "_lib", Lib())
+    monkeypatch.setattr(moe, "_ptr", lambda t: None if t is None else t.data_ptr())
+    monkeypatch.setattr(torch.cuda, "stream", use)
+    for name, f in (("empty", empty), ("empty_like", empty_like)):
+        monkeypatch.setattr(torch, name,
+                            lambda *a, f=f, **kw: allocs.append(stack[-1] if stack else None) or f(*a, **kw))
+    return allocs, launches
+
+
+def _block():
+    bf = torch.bfloat16
+    z = lambda *s, t=bf: torch.zeros(s, dtype=t)
+    return dict(x=z(T, D), w_router=z(E, D), wg=z(E, I, D), wu=z(E, I, D), wd=z(E, D, I), s_wg=z(I, D), s_wu=z(I, D),
+                s_wd=z(D, I))
+
+
+def _calls():
+    p = moe.Problem.make(T, D, E, K, I, I, "bf16", "bf16")
+    b = _block()
+    x = b["x"]
+    rows = torch.zeros((ROWS, D), dtype=torch.bfloat16)
+    ids, tw = torch.zeros((T, K), dtype=torch.int32), torch.zeros((T, K))
+    offs = torch.zeros(E + 2, dtype=torch.int32)
+    W = [b[n] for n in ("wg", "wu", "wd", "s_wg", "s_wu", "s_wd")]
+    codes = [torch.zeros(t.shape[:-1] + (t.shape[-1] // 2,), dtype=torch.uint8) for t in W]
+    scales = torch.full((sum(t.numel() // 32 for t in W),), 127, dtype=torch.uint8)
+    p4 = moe.Problem.make(T, D, E, K, I, I, "bf16", "mx4")
+    return {
+        "router_topk": lambda s: moe.router_topk(p, x, b["w_router"], stream=s),
+        "permute": lambda s: moe.permute(p, x, ids, tw, stream=s),
+        "expert_ffn": lambda s: moe.expert_ffn(p, rows, offs, *W, stream=s),
+        "expert_ffn, 4-bit": lambda s: moe.expert_ffn(p4, rows, offs, *codes, scales=scales, stream=s),
+        "combine": lambda s: moe.combine(p, rows, ids, tw, offs, stream=s),
+        "layer_forward": lambda s: moe.layer_forward(p, x, b["w_router"], None, *W, stream=s),
+        "block_forward": lambda s: moe.block_forward(p, x, b["w_router"], None, *W, stream=s),
+        "decode_forward": lambda s: moe.decode_forward(p, x, b["w_router"], None, *W, stream=s),
+        "rmsnorm": lambda s: moe.rmsnorm(p, x, torch.zeros(D, dtype=torch.bfloat16), stream=s),
+        "ep_expand_ids": lambda s: moe.ep_expand_ids(torch.zeros(E, dtype=torch.int32), 1, E, 5, stream=s),
+        "quantize_mx4": lambda s: moe.quantize_mx4(x, stream=s),
+        "dequantize_mx4": lambda s: moe.dequantize_mx4(codes[0], scales[:E * I * D // 32], stream=s),
+    }
+
+
+@pytest.mark.parametrize("name", list(_calls()))
+def test_a_call_allocates_on_the_stream_it_runs_on(name, recorded):
+    allocs, launches = recorded
+    s = Stream(41)
+    calls = _calls()
+    allocs.clear()
+    calls[name](s)
+    assert allocs and all(a is s for a in allocs), allocs
+    assert len(launches) == 1 and launches[0][1] == 41, launches
