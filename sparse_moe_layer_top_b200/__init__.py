@@ -683,7 +683,7 @@ def _decode(prob, x, w_router, bias, wg, wu, wd, s_wg, s_wu, s_wd, scales, norm_
 class MoELayer:
     """One block's weights plus a workspace sized for up to `max_tokens` tokens.
     Calling it runs the fused forward; ``decode`` the latency form for a few
-    tokens, in a workspace of its own."""
+    tokens."""
 
     def __init__(self, d, E, k, I, I_s, w_router, wg, wu, wd, s_wg=None, s_wu=None, s_wd=None, bias=None,
                  scales=None, act="bf16", w="bf16", max_tokens=0, norm_weight=None, norm_eps=1e-6,
@@ -696,7 +696,6 @@ class MoELayer:
                      shared_gate)
         self.device = wg.device
         self.ws = None
-        self.ws_decode = None
         if max_tokens:
             self._reserve(max_tokens)
 
@@ -720,18 +719,15 @@ class MoELayer:
                         shared_gate, y, topk_ids, topk_w, self.ws, stream, block)
 
     def decode(self, x, y=None, topk_ids=None, topk_w=None, stream=None):
-        """The block on x [T, d], T <= DECODE_MAX_T, in the latency form (decode_forward)."""
+        """The block on x [T, d], T <= DECODE_MAX_T, in the latency form (decode_forward).
+        The workspace is each call's own, from the pool of its stream or,
+        under capture, of its graph: calls on several streams may run at once."""
         prob = self.problem(x.shape[0])
         _need_tokens(prob, x, y, topk_ids, topk_w)
-        n = decode_workspace_size(prob)
-        if self.ws_decode is None or self.ws_decode.numel() < n:
-            # for the largest batch at once: a captured graph keeps its workspace
-            most = max(n, decode_workspace_size(self.problem(DECODE_MAX_T)), 1)
-            self.ws_decode = torch.empty(most, dtype=torch.uint8, device=self.device)
         w_router, bias, wg, wu, wd, s_wg, s_wu, s_wd, scales = self.w
         norm_weight, norm_eps, shared_gate = self.opts
         return _decode(prob, x, w_router, bias, wg, wu, wd, s_wg, s_wu, s_wd, scales, norm_weight, norm_eps,
-                       shared_gate, y, topk_ids, topk_w, self.ws_decode, stream)
+                       shared_gate, y, topk_ids, topk_w, None, stream)
 
     @classmethod
     def from_inputs(cls, inp, max_tokens=0):

@@ -51,3 +51,27 @@ def test_calls_without_a_workspace_on_a_side_stream(w):
             torch.cuda.synchronize()
             assert torch.equal(got, want)
     assert moe.device_status()[0] == 0
+
+
+@pytest.mark.parametrize("w", ["bf16", "mx4"])
+def test_one_layers_decode_on_two_streams_and_in_a_graph_at_once(w):
+    inp, W, scales = _inputs(w)
+    layer = moe.MoELayer(D, E, K, I, I_S, inp.w_r, *W, scales=scales, w=w)
+    xs = [inp.x[:1], inp.x[1:12], inp.x[12:15].clone()]
+    want = [layer.decode(x) for x in xs]
+    torch.cuda.synchronize()
+    sa, sb, sc = (torch.cuda.Stream() for _ in range(3))
+    y = torch.empty_like(want[2])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=sc):
+        layer.decode(xs[2], y, stream=sc)
+    for _ in range(20):
+        y.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(sc):
+            g.replay()
+        a, b = layer.decode(xs[0], stream=sa), layer.decode(xs[1], stream=sb)
+        _overwrite(moe.decode_workspace_size(layer.problem(16)))
+        torch.cuda.synchronize()
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1]) and torch.equal(y, want[2])
+    assert moe.device_status()[0] == 0

@@ -94,3 +94,20 @@ def test_a_call_allocates_on_the_stream_it_runs_on(name, recorded):
     calls[name](s)
     assert allocs and all(a is s for a in allocs), allocs
     assert len(launches) == 1 and launches[0][1] == 41, launches
+
+
+def _layer(**kw):
+    b = _block()
+    return moe.MoELayer(D, E, K, I, I, *[b[n] for n in ("w_router", "wg", "wu", "wd", "s_wg", "s_wu", "s_wd")], **kw)
+
+
+def test_decode_of_a_layer_has_a_workspace_of_its_own_on_every_stream(recorded):
+    allocs, launches = recorded
+    layer = _layer()
+    x, y = torch.zeros((3, D), dtype=torch.bfloat16), torch.zeros((3, D), dtype=torch.bfloat16)
+    s1, s2 = Stream(41), Stream(42)
+    allocs.clear()
+    for s in (s1, s2, s1):
+        layer.decode(x, y, stream=s)
+    assert allocs == [s1, s2, s1]
+    assert [l[1] for l in launches] == [41, 42, 41]
