@@ -75,3 +75,34 @@ def test_one_layers_decode_on_two_streams_and_in_a_graph_at_once(w):
         torch.cuda.synchronize()
         assert torch.equal(a, want[0]) and torch.equal(b, want[1]) and torch.equal(y, want[2])
     assert moe.device_status()[0] == 0
+
+
+@pytest.mark.parametrize("w", ["bf16", "mx4"])
+def test_a_layers_forward_on_side_streams_and_in_a_graph(w):
+    """One layer: a first call on a side stream, calls on two streams in turn, and
+    a captured one that stays right after the layer's workspace has grown."""
+    inp, W, scales = _inputs(w)
+    layer = moe.MoELayer(D, E, K, I, I_S, inp.w_r, *W, scales=scales, w=w)
+    small = inp.x[:40].clone()
+    ref = moe.MoELayer(D, E, K, I, I_S, inp.w_r, *W, scales=scales, w=w, max_tokens=T)
+    want, want_small = ref(inp.x), ref(small)
+    torch.cuda.synchronize()
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    got = layer(small, stream=sa)
+    _overwrite(moe.workspace_size(layer.problem(40)))
+    torch.cuda.synchronize()
+    assert torch.equal(got, want_small)
+    y = torch.empty_like(small)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=sa):
+        layer(small, y, stream=sa)
+    big = layer(inp.x)  # the workspace grows
+    _overwrite(moe.workspace_size(layer.problem(40)))
+    y.zero_()
+    torch.cuda.synchronize()
+    g.replay()
+    outs = [layer(inp.x, stream=s) for s in (sa, sb, sa, sb)]
+    torch.cuda.synchronize()
+    assert torch.equal(big, want) and torch.equal(y, want_small)
+    assert all(torch.equal(o, want) for o in outs)
+    assert moe.device_status()[0] == 0

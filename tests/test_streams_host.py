@@ -111,3 +111,60 @@ def test_decode_of_a_layer_has_a_workspace_of_its_own_on_every_stream(recorded):
         layer.decode(x, y, stream=s)
     assert allocs == [s1, s2, s1]
     assert [l[1] for l in launches] == [41, 42, 41]
+
+
+def test_a_layers_workspace_is_ordered_between_streams_and_never_a_graphs(recorded, monkeypatch):
+    """One buffer, and a call on another stream waits for the last one's; a
+    captured call allocates for itself, so that a later growth takes nothing
+    from its graph."""
+    allocs, launches = recorded
+    waits, state = [], {"capturing": False}
+
+    class S(Stream):
+        def wait_stream(self, other):
+            waits.append((self.cuda_stream, other.cuda_stream))
+
+    home, s1, s2 = S(40), S(41), S(42)
+    for s in (home, s1, s2):
+        s.device = torch.device("cuda", 0)
+    enter = torch.cuda.stream
+    stack = [home]
+
+    @contextlib.contextmanager
+    def use(stream):
+        stack.append(stream)
+        with enter(stream):
+            yield
+        stack.pop()
+
+    monkeypatch.setattr(torch.cuda, "stream", use)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: stack[-1])
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: state["capturing"])
+    monkeypatch.setattr(moe, "_stream", lambda stream=None: (stream or stack[-1]).cuda_stream)
+    monkeypatch.setattr(moe, "_device", lambda *a, **kw: torch.device("cuda", 0))
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: None)
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, device=None, **kw: empty(*a, **kw))
+    layer = _layer()
+    layer.device = torch.device("cuda", 0)
+    layer._reserve(T)
+    ws = layer.ws
+    x, y = torch.zeros((T, D), dtype=torch.bfloat16), torch.zeros((T, D), dtype=torch.bfloat16)
+    used = []
+    monkeypatch.setattr(moe, "_forward_call", lambda *a: used.append((a[17], a[18])))
+    layer(x, y)
+    layer(x, y, stream=s1)
+    layer(x, y, stream=s1)
+    layer(x, y, stream=s2)
+    assert [u[0] is ws for u in used] == [True] * 4 and [u[1] for u in used] == [None, s1, s1, s2]
+    assert waits == [(41, 40), (42, 41)]
+    used.clear()
+    state["capturing"] = True
+    allocs.clear()
+    layer(x, y, stream=s1)
+    assert used[0][0] is not ws and allocs == [s1] and layer.ws is ws and waits[2:] == []
+    state["capturing"] = False
+    x = torch.zeros((4 * T, D), dtype=torch.bfloat16)
+    layer(x, torch.zeros_like(x), stream=s1)  # grows on the stream that uses it
+    assert layer.ws is not ws and allocs[1:] == [s1] and layer.ws_stream is s1 and waits[2:] == []
