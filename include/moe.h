@@ -206,10 +206,9 @@ MOE_API moe_status moe_rmsnorm(const moe_problem* p, const void* x, const void* 
  * experts' weight bytes plus about fifteen microseconds.  bf16 activations;
  * BF16, FP8_E4M3_B128 or MXFP4_B32 weights.  Sums are fp32 throughout.  The
  * SwiGLU activation, already multiplied by the routing weight, enters the down
- * projection rounded once: to bf16 (BF16 weights), to the sum of two E4M3 terms
- * (E4M3 weights; x enters its products the same way) or to fp16 (4-bit
- * weights; x too, exactly but for values 2^-31 of its 128-column block's
- * largest), the last two under a power of two per 128 columns.  The down
+ * projection rounded once: to bf16 (BF16 weights), or to fp16 under a power of two
+ * per 128 columns (E4M3 and 4-bit weights; x enters its products the same way,
+ * exactly but for values below 2^-31 of its 128-column block's largest).  The down
  * projection is one sum over the token's experts, rounded once to y, so results
  * differ from moe_block_forward's in rounding only; they are reproducible bit
  * for bit.  An infinity or a NaN in the weights of an expert reaches only the

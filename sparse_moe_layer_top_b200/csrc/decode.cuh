@@ -12,7 +12,7 @@
 //      CTA), and lists the active experts;
 //   2. gate/up: h[t, slot, f] = w * SiLU(W_g[f] x_t) * (W_u[f] x_t), units of 16
 //      features of one expert.  The routing weight w is applied here, so that
-//   -- grid barrier (E4M3, mx4: h is scaled like x, and another barrier) --
+//   -- grid barrier (E4M3, mx4: h is scaled to f16 like x, and another barrier) --
 //   3. the down projection is ONE sum per output: y[t, n] = sum over the active
 //      experts and their features of W_d[n, f] h[t, slot, f], units of 16 outputs
 //      over all experts; fp32 throughout, rounded once, no atomics: reproducible.
@@ -25,13 +25,13 @@
 //     in shared memory by cp.async, kDecStages stages of two pieces deep, over unit
 //     boundaries and, for the down projection's first pieces, from before the barrier:
 //     no block-wide step waits for memory.
-//   instructions: bf16 weights go to m16n8k16 as they are, E4M3 codes to m16n8k32 as
-//     they are, mx4 codes are converted to f16 two at a time.  For the last two the
-//     tokens' values are scaled by a power of two per 128 columns: for mx4 to f16, the
-//     largest in [2^14, 2^15), which holds a bf16 exactly down to 2^-31 of it; for E4M3
-//     to the sum of two E4M3 terms, x = s (hi + lo), the largest in (224, 448]: hi has
-//     four significant bits, lo the rest, exact down to 2^-9 of that largest and off by
-//     at most 2^-17 of it below.
+//   instructions: bf16 weights go to m16n8k16 as they are, E4M3 and mx4 codes are
+//     converted to f16 (exactly) two at a time.  For those the tokens' values are f16
+//     under a power of two per 128 columns, the largest in [2^14, 2^15), which holds a
+//     bf16 exactly down to 2^-31 of it: a channel far above the others costs them nothing.
+//     (E4M3 codes as they are, with x and h as two E4M3 terms under one scale, held the
+//     others to 2^-18 of it, and were slower too: 4 tokens at d = 4096, I = 1536, E = 64,
+//     k = 6 103 us against 97, 16 tokens 195 against 181.)
 //     8 tokens at d = 8192, I = 2048, E = 512, k = 10, mx4: with the codes converted to
 //     bf16 by bit moves (20 operations per 8 codes at half rate) and fragments loaded
 //     straight into registers 852 us.
@@ -76,7 +76,7 @@ struct DecodeArgs {
   const uint8_t* sc[6]; // scale parts: gate, up, down, shared gate, up, down
   float* gate;          // [T] weight of the shared expert, or NULL (1)
   bf16* xn;             // [T, d] the normalised input (bf16 weights with a norm)
-  uint8_t* xq;          // [T][d / 32][64] x, scaled: f16 (mx4) or E4M3 terms (dec_term_place)
+  uint8_t* xq;          // [T][d / 32][64] x as scaled f16 (dec_split)
   float* xsc;           // [d / 128][kDecodeMaxT] its scales
   float* logits;        // [splits][T][E] partial logits
   int splits;
@@ -103,31 +103,12 @@ struct DecW {
   static __device__ __forceinline__ int64_t bytes(int64_t n) { return W == kDecBf16 ? 2 * n : W == kDecFp8 ? n : n >> 1; }
 };
 
-// Place of element e (0..31) of a 32-column block in its 64 bytes of E4M3 terms: lane
-// c of a lane group takes 16 bytes, the hi terms of columns 4c.. and 16 + 4c.., then
-// their lo terms.  (hi; the lo term is 8 bytes further)
-__device__ __forceinline__ int dec_term_place(int e) { return ((e & 15) >> 2) * 16 + (e >> 4) * 4 + (e & 3); }
-
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_e4m3_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                               uint32_t b0, uint32_t b1) {  // d = A * B
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -227,6 +208,15 @@ __device__ __forceinline__ void mx4_to_f16(uint32_t q, uint32_t (&h)[4]) {
       : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
       : "r"(q));
 }
+// Four E4M3 codes -> two f16 pairs of consecutive values.
+__device__ __forceinline__ void e4m3_to_f16(uint32_t q, uint32_t (&h)[2]) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(h[0]), "=r"(h[1])
+      : "r"(q));
+}
 // Some byte of w is 0 or 255.
 __device__ __forceinline__ bool has_edge_byte(uint32_t w) {
   return (((w - 0x01010101u) & ~w) | ((~w - 0x01010101u) & w)) & 0x80808080u;
@@ -245,22 +235,27 @@ __device__ __forceinline__ void dec_mma(float (&acc)[NB][4], const DecFrag& f, c
       }
   } else if (W == kDecFp8) {
     const float sc = __uint_as_float(f.s0);
+    float p[NB][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // 16 columns
+      uint32_t l[2], h[2];
+      e4m3_to_f16(f.lo[i], l);
+      e4m3_to_f16(f.hi[i], h);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const uint4 b = bw[nb][(i >> 1) % DecW<W>::BV];
+        if (i == 0) mma_f16_first(p[nb], l[0], h[0], l[1], h[1], b.x, b.y);
+        else mma_f16(p[nb], l[0], h[0], l[1], h[1], i & 1 ? b.z : b.x, i & 1 ? b.w : b.y);
+      }
+    }
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-        float p[4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint4 b = bw[nb][i % DecW<W>::BV];
-          if (i == 0) mma_e4m3_first(p, f.lo[0], f.hi[0], f.lo[1], f.hi[1], b.x, b.y);
-          else mma_e4m3(p, f.lo[2 * i], f.hi[2 * i], f.lo[2 * i + 1], f.hi[2 * i + 1], b.x, b.y);
-          mma_e4m3(p, f.lo[2 * i], f.hi[2 * i], f.lo[2 * i + 1], f.hi[2 * i + 1], b.z, b.w);
-        }
-        const float s0 = sc * xs[nb].x, s1 = sc * xs[nb].y;
-        acc[nb][0] = fmaf(s0, p[0], acc[nb][0]);
-        acc[nb][1] = fmaf(s1, p[1], acc[nb][1]);
-        acc[nb][2] = fmaf(s0, p[2], acc[nb][2]);
-        acc[nb][3] = fmaf(s1, p[3], acc[nb][3]);
-      }
+      const float s0 = sc * xs[nb].x, s1 = sc * xs[nb].y;
+      acc[nb][0] = fmaf(s0, p[nb][0], acc[nb][0]);
+      acc[nb][1] = fmaf(s1, p[nb][1], acc[nb][1]);
+      acc[nb][2] = fmaf(s0, p[nb][2], acc[nb][2]);
+      acc[nb][3] = fmaf(s1, p[nb][3], acc[nb][3]);
+    }
   } else {
     float s0[4], s8[4];
     if (__any_sync(0xffffffffu, has_edge_byte(f.s0) || has_edge_byte(f.s8))) {
@@ -319,8 +314,10 @@ __device__ __forceinline__ void dec_tok(uint4 (&bw)[DecW<W>::BV], const uint8_t*
 }
 
 // -------------------------------------------------------------- scaled tokens
-// Four consecutive values a lane, 128 columns a warp: scaled to q (the 128 columns'
+// Four consecutive values a lane, 128 columns a warp: as f16 to q (the 128 columns'
 // 256 bytes), the scale to *sc.  A block holding an infinity or a NaN becomes NaN.
+// A lane c of a product takes 16 bytes of each 32 columns: mx4 columns 8c .. 8c + 7 (the
+// codes of a 32-bit word), E4M3 4c .. 4c + 3 and 16 + 4c .. (a word each).
 template <int W>
 __device__ __forceinline__ void dec_split(const float (&v)[4], uint8_t* q, float* sc, int lane) {
   uint32_t amax = 0;
@@ -328,29 +325,13 @@ __device__ __forceinline__ void dec_split(const float (&v)[4], uint8_t* q, float
   for (int i = 0; i < 4; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);
   amax = __reduce_max_sync(0xffffffffu, amax);
   const float nan = __uint_as_float(0x7fffffffu);
-  if (W == kDecMx4) {
-    const uint32_t e = max(amax >> 23, 15u);
-    const float inv = e == 255u ? nan : __uint_as_float((268u - e) << 23);  // 2^(14 - exponent)
-    const __half2 a = __floats2half2_rn(v[0] * inv, v[1] * inv), b = __floats2half2_rn(v[2] * inv, v[3] * inv);
-    *reinterpret_cast<uint2*>(q + lane * 8) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-    if (lane == 0) *sc = e == 255u ? nan : __uint_as_float((e - 14u) << 23);
-  } else {
-    const uint32_t b = mx_split_byte(amax);
-    const float inv = mx_split_inv(b);
-    uint32_t h[2], l[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float a0 = v[2 * i] * inv, a1 = v[2 * i + 1] * inv;
-      h[i] = e4m3x2(a0, a1);
-      const float2 w = e4m3x2_value(h[i]);
-      l[i] = e4m3x2(a0 - w.x, a1 - w.y);
-    }
-    uint8_t* o = q + (lane >> 3) * 64 + dec_term_place((lane & 7) * 4);
-    *reinterpret_cast<uint32_t*>(o) = h[0] | h[1] << 16;
-    *reinterpret_cast<uint32_t*>(o + 8) = l[0] | l[1] << 16;
-    if (lane == 0) *sc = b == 255u ? nan : __uint_as_float(b << 23);
-  }
+  const uint32_t e = max(amax >> 23, 15u);
+  const float inv = e == 255u ? nan : __uint_as_float((268u - e) << 23);  // 2^(14 - exponent)
+  const __half2 a = __floats2half2_rn(v[0] * inv, v[1] * inv), b = __floats2half2_rn(v[2] * inv, v[3] * inv);
+  const int at = W == kDecMx4 ? lane * 8 : (lane >> 3) * 64 + (lane & 3) * 16 + (lane >> 2 & 1) * 8;
+  *reinterpret_cast<uint2*>(q + at) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  if (lane == 0) *sc = e == 255u ? nan : __uint_as_float((e - 14u) << 23);
 }
 
 // Barrier of the cooperative grid, in two halves: writes before a CTA's arrival are
@@ -710,7 +691,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a
     const int kw = kw1, team = warp / kw, tw = warp % kw, tpc = kDecodeWarps / kw;
     const int units = f_s + n_act * f_r, step = gridDim.x * tpc;
     const uint8_t* xin = DecW<W>::SCALED ? a.xq : reinterpret_cast<const uint8_t*>(a.gamma ? a.xn : a.x);
-    const int64_t xrow = (int64_t)a.d * 2;  // bytes of a token's row, as bf16 or as terms
+    const int64_t xrow = (int64_t)a.d * 2;  // bytes of a token's row, bf16 or f16
     const int64_t step8 = DecW<W>::bytes((int64_t)8 * a.d);
     const uint32_t lane_at = dec_unit(g, c);
     int iu = tw < nch_d ? blockIdx.x + gridDim.x * team : units, ik = tw;

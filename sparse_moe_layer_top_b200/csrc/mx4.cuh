@@ -76,8 +76,8 @@ __device__ __forceinline__ float mx4_value(const mx4* codes, const uint8_t* scal
 }
 
 // ---------------------------------------------------------------- E4M3 terms
-// The kernels that multiply 4-bit (or E4M3) weights by bf16 values take a value as
-// the sum of two E4M3 terms under one power-of-two scale per block of columns.
+// The expert GEMMs on 4-bit weights take a bf16 value as the sum of two E4M3 terms
+// under one power-of-two scale per block of columns (tc_mx4.cuh).
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {  // a in the low byte
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(r) : "f"(a), "f"(b));

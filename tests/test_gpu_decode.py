@@ -9,10 +9,11 @@ bf16, relative):
   h = w * silu(g) * u inherits g's and u's (|silu'| <= 1.1), the fast exponential
   and the divisions (2^-18 together), the routing weight's own error, and with
   bf16 weights one rounding to bf16; y its sum's, plus one rounding to bf16.
-With E4M3 weights x and h enter their products as two E4M3 terms under one scale
-per 128 columns: off by at most half of the second term's smallest spacing, 2^-10,
-where the largest of the 128 is above 224, or 2^-8 relative (a term's half step,
-twice); with 4-bit weights as f16 under such a scale: half of its smallest
+With E4M3 weights the bound allows x and h two E4M3 terms under one scale per 128
+columns: off by at most half of the second term's smallest spacing, 2^-10, where
+the largest of the 128 is above 224, or 2^-8 relative (a term's half step,
+twice).  (They are held closer, as with 4-bit weights: test_gpu_decode_outliers.py.)
+With 4-bit weights they are f16 under such a scale: half of its smallest
 spacing, 2^-25, where the largest is at least 2^14, or 2^-11 relative.  x, a
 bf16, is held exactly where that relative error is the larger.
 The routing weight: a logit's error moves a softmax weight by at most twice
