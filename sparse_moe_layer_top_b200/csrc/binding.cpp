@@ -119,6 +119,13 @@ bool weights(Call& c, const moe_problem& p, PyObject* const* o, Weights* w) {
 
 PyObject* none() { Py_RETURN_NONE; }
 
+// The interpreter's lock is given up around the allocations and the launches, as a
+// ctypes call gives it up: a launch may wait for a full queue.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 // A status as an int, else `result` (a new reference).
 template <typename F>
 PyObject* finish(int status, F result) {
@@ -146,9 +153,13 @@ PyObject* quantize(PyObject* const* a) {
   void* scales = c.need(a[2], batch * ss[ss.size() - 3] * ss[ss.size() - 2] * 512, at::kByte, 512, true);
   if (!c.ok) return none();
   at::Tensor tc, ts;
-  if (a[1] == Py_None) codes = (tc = c.empty(cs, at::kByte)).data_ptr();
-  if (a[2] == Py_None) scales = (ts = c.empty(ss, at::kByte)).data_ptr();
-  const int s = f_quantize(x->data_ptr(), f32 ? MOE_F32 : MOE_BF16, batch, rows, cols, codes, scales, c.stream());
+  int s;
+  {
+    Unlocked u;
+    if (a[1] == Py_None) codes = (tc = c.empty(cs, at::kByte)).data_ptr();
+    if (a[2] == Py_None) scales = (ts = c.empty(ss, at::kByte)).data_ptr();
+    s = f_quantize(x->data_ptr(), f32 ? MOE_F32 : MOE_BF16, batch, rows, cols, codes, scales, c.stream());
+  }
   return finish(s, [&] {
     PyObject* r = PyTuple_New(2);
     PyTuple_SET_ITEM(r, 0, given(a[1], tc));
@@ -178,9 +189,13 @@ PyObject* dequantize(PyObject* const* a) {
   void* out = c.need(a[2], batch * rows * cols, type, cols, true);
   if (!c.ok) return none();
   at::Tensor to;
-  if (a[2] == Py_None) out = (to = c.empty(os, type)).data_ptr();
-  const int s = f_dequantize(q->data_ptr(), scales, batch, rows, cols, type == at::kFloat ? MOE_F32 : MOE_BF16, out,
-                             c.stream());
+  int s;
+  {
+    Unlocked u;
+    if (a[2] == Py_None) out = (to = c.empty(os, type)).data_ptr();
+    s = f_dequantize(q->data_ptr(), scales, batch, rows, cols, type == at::kFloat ? MOE_F32 : MOE_BF16, out,
+                     c.stream());
+  }
   return finish(s, [&] { return given(a[2], to); });
 }
 
@@ -199,10 +214,14 @@ PyObject* expert_ffn(PyObject* const* a) {
   const at::Tensor* ws = c.tensor(a[11], true);
   if (!c.ok) return none();
   at::Tensor ty, tw;
-  if (a[10] == Py_None) y = (ty = c.empty({tx->size(0), p.d}, at::kBFloat16)).data_ptr();
-  if (!ws) ws = &(tw = c.empty({(int64_t)std::max<size_t>(f_stage_ws(&p), 1)}, at::kByte));
-  const int s = f_expert_ffn(&p, x, (const int32_t*)offs, w.wg, w.wu, w.wd, w.sg, w.su, w.sd, w.scales, y,
-                             ws->data_ptr(), ws->nbytes(), c.stream());
+  int s;
+  {
+    Unlocked u;
+    if (a[10] == Py_None) y = (ty = c.empty({tx->size(0), p.d}, at::kBFloat16)).data_ptr();
+    if (!ws) ws = &(tw = c.empty({(int64_t)std::max<size_t>(f_stage_ws(&p), 1)}, at::kByte));
+    s = f_expert_ffn(&p, x, (const int32_t*)offs, w.wg, w.wu, w.wd, w.sg, w.su, w.sd, w.scales, y, ws->data_ptr(),
+                     ws->nbytes(), c.stream());
+  }
   return finish(s, [&] { return given(a[10], ty); });
 }
 
@@ -231,10 +250,14 @@ PyObject* decode(PyObject* const* a) {
   }
   if (!c.ok) return none();
   at::Tensor ty, tws;
-  if (a[14] == Py_None) y = (ty = c.empty({p.T, d}, at::kBFloat16)).data_ptr();
-  if (!ws) ws = &(tws = c.empty({(int64_t)std::max<size_t>(f_decode_ws(&p), 1)}, at::kByte));
-  const int s = f_decode(&p, &opt, x, wr, (const float*)bias, w.wg, w.wu, w.wd, w.sg, w.su, w.sd, w.scales, y,
-                         (int32_t*)ids, (float*)tw, ws->data_ptr(), ws->nbytes(), c.stream());
+  int s;
+  {
+    Unlocked u;
+    if (a[14] == Py_None) y = (ty = c.empty({p.T, d}, at::kBFloat16)).data_ptr();
+    if (!ws) ws = &(tws = c.empty({(int64_t)std::max<size_t>(f_decode_ws(&p), 1)}, at::kByte));
+    s = f_decode(&p, &opt, x, wr, (const float*)bias, w.wg, w.wu, w.wd, w.sg, w.su, w.sd, w.scales, y, (int32_t*)ids,
+                 (float*)tw, ws->data_ptr(), ws->nbytes(), c.stream());
+  }
   return finish(s, [&] { return given(a[14], ty); });
 }
 

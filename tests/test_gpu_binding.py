@@ -132,3 +132,29 @@ def test_the_current_stream_is_used():
         v = moe.dequantize_mx4(c, sc)
     s.synchronize()
     assert (v == 3).all()
+
+
+def test_a_call_gives_up_the_interpreters_lock():
+    """In the place of the library's entry points a function that says whether its
+    thread holds the lock: 0 (the status of success) when it does not."""
+    import ctypes
+    inp, ws, scales = _weights("mx4")
+    prob = moe.Problem.make(12, 256, 6, 2, 128, 128, "bf16", "mx4")
+    rows, offs = torch.zeros(36, 256, dtype=torch.bfloat16, device="cuda"), torch.zeros(8, dtype=torch.int32, device="cuda")
+    x = torch.zeros(8, 64, device="cuda")
+    codes, tiles = moe.quantize_mx4(x)
+    stage, few = (torch.empty(f(prob), dtype=torch.uint8, device="cuda")
+                  for f in (moe.stage_workspace_size, moe.decode_workspace_size))
+    m = moe._fast()
+    names = ("moe_mx4_quantize", "moe_mx4_dequantize", "moe_expert_ffn", "moe_stage_workspace_size",
+             "moe_decode_workspace_size", "moe_decode_forward")
+    real = [ctypes.cast(getattr(moe.lib(), n), ctypes.c_void_p).value for n in names]
+    held = ctypes.cast(ctypes.pythonapi.PyGILState_Check, ctypes.c_void_p).value
+    m.bind(*[r if n.endswith("_size") else held for n, r in zip(names, real)])
+    try:
+        got = [m.quantize(x, None, None), m.dequantize(codes, tiles, None, True),
+               m.expert_ffn(prob, rows, offs, *ws, scales, None, stage),
+               m.decode(prob, inp.x, inp.w_r, None, *ws, scales, None, 1e-6, None, None, None, None, few)]
+    finally:
+        m.bind(*real)
+    assert not any(isinstance(g, int) or g is None for g in got), got
