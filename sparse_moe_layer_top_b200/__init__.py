@@ -740,9 +740,14 @@ class MoELayer:
         The workspace is each call's own, from the pool of its stream or,
         under capture, of its graph: calls on several streams may run at once."""
         prob = self.problem(x.shape[0])
-        _need_tokens(prob, x, y, topk_ids, topk_w)
         w_router, bias, wg, wu, wd, s_wg, s_wu, s_wd, scales = self.w
         norm_weight, norm_eps, shared_gate = self.opts
+        if stream is None:
+            r = _fast_call("decode", prob, x, w_router, bias, wg, wu, wd, s_wg, s_wu, s_wd, scales, norm_weight,
+                           norm_eps, shared_gate, y, topk_ids, topk_w, None)
+            if r is not None:
+                return r
+        _need_tokens(prob, x, y, topk_ids, topk_w)
         return _decode(prob, x, w_router, bias, wg, wu, wd, s_wg, s_wu, s_wd, scales, norm_weight, norm_eps,
                        shared_gate, y, topk_ids, topk_w, None, stream)
 

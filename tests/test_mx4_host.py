@@ -189,3 +189,22 @@ def test_split_scales_takes_scale_tiles():
         assert (out[r].reshape(-1, per) == out[r].reshape(-1, per)[:, :1]).all()
     with pytest.raises(ValueError, match="scales hold"):
         ep.split_scales(0, G, E, d, I, I_s, tag[:-1])
+
+
+def test_decode_of_a_layer_makes_the_calls_decode_forward_makes(monkeypatch):
+    """The regular call in C++, with the same arguments as decode_forward's."""
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    W = [z(4, 128, 128), z(4, 128, 128), z(4, 128, 128), z(128, 128), z(128, 128), z(128, 128)]
+    bias, gamma, gate = torch.zeros(4), z(128), z(128)
+    layer = moe.MoELayer(128, 4, 2, 128, 128, z(4, 128), *W, bias=bias, norm_weight=gamma, norm_eps=1e-5,
+                         shared_gate=gate)
+    calls = []
+    monkeypatch.setattr(moe, "_fast_call", lambda *a: calls.append(a) or "y")
+    x, y = z(3, 128), z(3, 128)
+    ids, tw = torch.zeros((3, 2), dtype=torch.int32), torch.zeros((3, 2))
+    assert layer.decode(x, y, ids, tw) == "y"
+    assert moe.decode_forward(layer.problem(3), x, layer.w[0], bias, *W, norm_weight=gamma, norm_eps=1e-5,
+                              shared_gate=gate, y=y, topk_ids=ids, topk_w=tw) == "y"
+    (a, b) = calls
+    assert bytes(a[1]) == bytes(b[1]) and len(a) == len(b)
+    assert all(p is q for p, q in zip(a[:1] + a[2:], b[:1] + b[2:]))
