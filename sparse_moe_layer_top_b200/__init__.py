@@ -25,6 +25,7 @@ several GPUs (expert parallelism).
 import contextlib
 import ctypes
 import os
+import warnings
 
 import torch
 
@@ -142,12 +143,15 @@ _binding = False
 def _fast():
     """The binding's C++ side (csrc/binding.cpp), which makes the regular calls of
     the latency-bound entry points without the checks below; None when it is not
-    built or cannot be loaded -- the calls then go through Python, with the same results."""
+    built or cannot be loaded -- the calls then go through Python, with the same
+    kernels and results, which a RuntimeWarning says once."""
     global _binding
     if _binding is False:
         try:
             from . import _moe_binding as m
-        except ImportError:
+        except ImportError as e:
+            warnings.warn("the binding's C++ side is not there (python -m sparse_moe_layer_top_b200.build): small calls "
+                          "take about 10 us longer on the host; %s" % e, RuntimeWarning, stacklevel=3)
             m = None
         if m is not None:
             L = lib()

@@ -208,3 +208,18 @@ def test_decode_of_a_layer_makes_the_calls_decode_forward_makes(monkeypatch):
     (a, b) = calls
     assert bytes(a[1]) == bytes(b[1]) and len(a) == len(b)
     assert all(p is q for p, q in zip(a[:1] + a[2:], b[:1] + b[2:]))
+
+
+def test_a_missing_cpp_side_is_reported_once(monkeypatch):
+    import sys
+    import warnings
+    monkeypatch.setitem(sys.modules, "sparse_moe_layer_top_b200._moe_binding", None)
+    monkeypatch.delattr(moe, "_moe_binding", raising=False)
+    monkeypatch.setattr(moe, "_binding", False)
+    with pytest.warns(RuntimeWarning, match="C\\+\\+ side"):
+        assert moe._fast() is None
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        assert moe._fast() is None
+        with pytest.raises(ValueError, match=ON_DEVICE):
+            moe.quantize_mx4(torch.zeros(4, 64))
