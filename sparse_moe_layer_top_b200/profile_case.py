@@ -35,6 +35,10 @@ def arg_parser():
 
 
 def main(argv=None):
+    ap = arg_parser()
+    a = ap.parse_args(argv)
+    if a.config and a.w == "mx4":
+        ap.error("--config runs a workload with its own weights; --w mx4 takes the sizes given here")
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     if root not in sys.path:
         sys.path.insert(0, root)
@@ -43,7 +47,6 @@ def main(argv=None):
     import moe_inputs
     import sparse_moe_layer_top_b200 as moe
 
-    a = arg_parser().parse_args(argv)
     torch.cuda.set_device(0)
     if a.config:
         inp = moe_inputs.make_config(a.config, seed=0, device="cuda")

@@ -223,3 +223,10 @@ def test_a_missing_cpp_side_is_reported_once(monkeypatch):
         assert moe._fast() is None
         with pytest.raises(ValueError, match=ON_DEVICE):
             moe.quantize_mx4(torch.zeros(4, 64))
+
+
+def test_profile_case_refuses_4_bit_weights_for_a_named_workload(capsys):
+    from sparse_moe_layer_top_b200 import profile_case
+    with pytest.raises(SystemExit):
+        profile_case.main(["--config", "qwen38max_decode_bf16", "--w", "mx4"])
+    assert "--w mx4" in capsys.readouterr().err
