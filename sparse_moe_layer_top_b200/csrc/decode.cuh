@@ -807,6 +807,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode(const DecodeArgs a
         const float w = sh ? (a.gate ? __ldg(a.gate + t) : 1.f) : s.w[t][j];
         const float hv = w * (vg / (1.f + __expf(-vg)) * vu);
         const int64_t at = ((int64_t)t * (a.k + 1) + j) * a.ldh + f;
+        // bf16 weights: h rounded to bf16, as the products of the fused forward take it.
+        // (As the sum of two bf16 terms the outputs were off by 0.0017 of their norm, their
+        // own rounding, in place of 0.0024, and 8 tokens at d = 4096, I = 1536, E = 64,
+        // k = 6 took 244 us in place of 234.)
         if (DecW<W>::SCALED) static_cast<float*>(a.h)[at] = hv;
         else static_cast<bf16*>(a.h)[at] = __float2bfloat16_rn(hv);
       }

@@ -59,3 +59,18 @@ def test_a_far_feature_of_h(T, d, I, I_s):
     _zero_columns(kw, ref, ("wd", "s_wd"), slice(7, None, 128))
     out = few._run(kw)
     few._check(out, few._reference(_bound_of_f16(kw), ref, out=out))
+
+
+def test_an_infinite_down_weight_gives_infinities():
+    T, E, k = 9, 12, 3
+    kw, ref = few._make(T, 256, E, k, 136, 72, "bf16", seed=60)
+    e = int(few._run(kw)[1][0, 0])
+    kw["wd"][e, 5, 7] = float("inf")
+    y, ids, _ = few._run(kw)
+    hit = (ids == e).any(1).cpu()
+    x, wg, wu = kw["x"].double().cpu(), ref[0][e, 7], ref[1][e, 7]
+    h = x @ wg * torch.sigmoid(x @ wg) * (x @ wu)
+    assert hit.any() and (y[~hit.cuda()].isfinite()).all()
+    assert torch.equal(y[hit.cuda(), 5].cpu().double(), torch.copysign(torch.full_like(h, float("inf")), h)[hit])
+    y[:, 5] = 0
+    assert y.isfinite().all()
