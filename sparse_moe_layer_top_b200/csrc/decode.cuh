@@ -463,20 +463,31 @@ __device__ __forceinline__ void dec_topk(const float* logits, int E, int k, int 
 }
 
 // -------------------------------------------------------------- norm, gate, logits
-// Eight values of x, normalised: v * r * (1 + gamma), rounded to bf16.
-__device__ __forceinline__ uint4 dec_norm8(uint4 x, uint4 gamma, float r) {
+// v * (r.x + r.y) * (1 + gamma), what each operation rounds off carried along: a value
+// that fp32 puts on the other side of the middle of two bf16 moves a logit by 2^-8 of
+// its term, and so which experts are taken.
+__device__ __forceinline__ float dec_norm(float v, float gamma, float2 r) {
+  const float t = 1.0f + gamma, tl = gamma - (t - 1.0f);
+  const float p = v * r.x, pl = fmaf(v, r.y, fmaf(v, r.x, -p));
+  const float q = p * t, s = q + fmaf(p, tl, fmaf(pl, t, fmaf(p, t, -q)));
+  return isfinite(q) ? s : q;
+}
+// Eight values of x, normalised and rounded to bf16.
+__device__ __forceinline__ uint4 dec_norm8(uint4 x, uint4 gamma, float2 r) {
   const uint32_t a[4] = {x.x, x.y, x.z, x.w}, g[4] = {gamma.x, gamma.y, gamma.z, gamma.w};
   uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    o[i] = pack_bf16x2(__uint_as_float(a[i] << 16) * r * (1.0f + __uint_as_float(g[i] << 16)),
-                       __uint_as_float(a[i] & 0xffff0000u) * r * (1.0f + __uint_as_float(g[i] & 0xffff0000u)));
+    o[i] = pack_bf16x2(dec_norm(__uint_as_float(a[i] << 16), __uint_as_float(g[i] << 16), r),
+                       dec_norm(__uint_as_float(a[i] & 0xffff0000u), __uint_as_float(g[i] & 0xffff0000u), r));
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 template <int W, int NB>
 __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode_route(const DecodeArgs a) {
   pdl_begin();  // after the previous kernel in the stream (programmatic launch)
-  __shared__ float s_r[kDecodeMaxT], s_part[kDecodeWarps];
+  __shared__ float2 s_r[kDecodeMaxT];  // 1 / rms and what its rounding to fp32 took off
+  __shared__ double s_sq[kDecodeWarps];
+  __shared__ float s_part[kDecodeWarps];
   __shared__ float red[kDecodeWarps][NB * 128];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;
@@ -486,28 +497,36 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode_route(const Decode
     int wpt = 16;  // warps of a token
     while (wpt * a.T > kDecodeWarps) wpt >>= 1;
     const int t = warp / wpt;
-    float ss = 0.f;
+    float ss = 0.f, sl = 0.f;  // the sum of squares, and what its additions rounded off
     if (t < a.T) {
       const uint4* row = reinterpret_cast<const uint4*>(a.x + (int64_t)t * a.d);
 #pragma unroll 4
       for (int j = warp % wpt * 32 + lane; j < a.d / 8; j += wpt * 32) {
         const uint4 v = __ldg(row + j);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        float s8 = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float p = __uint_as_float(w[i] << 16), q = __uint_as_float(w[i] & 0xffff0000u);
-          ss = fmaf(p, p, ss);
-          ss = fmaf(q, q, ss);
+          s8 = fmaf(p, p, s8);
+          s8 = fmaf(q, q, s8);
         }
+        const float sum = ss + s8, back = sum - ss;
+        sl += (ss - (sum - back)) + (s8 - back);
+        ss = sum;
       }
-      ss = dec_warp_sum(ss);
     }
-    if (lane == 0) s_part[warp] = ss;
+    double sq = isfinite(ss) ? (double)ss + sl : ss;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+    if (lane == 0) s_sq[warp] = sq;
     __syncthreads();
     if (tid < a.T) {
-      float v = 0.f;
-      for (int w = 0; w < wpt; ++w) v += s_part[tid * wpt + w];
-      s_r[tid] = 1.0f / sqrtf(v / (float)a.d + a.eps);
+      double v = 0.0;
+      for (int w = 0; w < wpt; ++w) v += s_sq[tid * wpt + w];
+      const double r = 1.0 / sqrt(v / a.d + a.eps);
+      const float hi = (float)r;
+      s_r[tid] = make_float2(hi, isfinite(hi) ? (float)(r - hi) : 0.f);
     }
     __syncthreads();
   }
