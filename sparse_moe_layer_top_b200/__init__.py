@@ -699,40 +699,52 @@ class MoELayer:
         _need_params(self.problem(0), w_router, bias, wg, wu, wd, s_wg, s_wu, s_wd, scales, norm_weight,
                      shared_gate)
         self.device = wg.device
-        self.ws = self.ws_stream = None  # the workspace, and the stream of the last call that used it
+        # the workspace, and the stream of the last call that used it
+        self.ws = self.ws_stream = self.ws_handle = None
         if max_tokens:
-            self._reserve(max_tokens)
+            self._reserve(self.problem(max_tokens))
 
     def problem(self, T):
         d, E, k, I, I_s, act, w = self.shape
         return Problem.make(T, d, E, k, I, I_s, act, w)
 
-    def _reserve(self, T, stream=None):
-        """The workspace of a call of T tokens on `stream`.  One buffer serves the
-        calls of every stream, so a call on another stream than the last one's
-        waits for that one's work.  None under capture: a graph that kept the
-        buffer would share it with eager calls, and outlive it when it grows; the
-        call's own allocation comes from the graph's pool instead."""
+    def _reserve(self, prob, stream=None):
+        """The workspace of a call on `stream`.  One buffer serves the calls of every
+        stream, so a call on another stream than the last one's waits for that one's
+        work.  None under capture: a graph that kept the buffer would share it with
+        eager calls, and outlive it when it grows; the call's own allocation comes
+        from the graph's pool instead."""
+        if stream is None and self.device.type == "cuda" and torch.cuda.current_device() == self.device.index:
+            return self._ordered(prob, None)
         if self.device.type != "cuda" or (stream is not None and stream.device != self.device):
             return self.ws  # (the call is refused)
         with _current(self.device), _alloc(stream):
-            if torch.cuda.is_current_stream_capturing():
-                return None
-            n = workspace_size(self.problem(T))
-            if self.ws is None or self.ws.numel() < n:
-                self.ws = None  # (freed first: the new one may take its place)
-                self.ws, self.ws_stream = torch.empty(n, dtype=torch.uint8, device=self.device), torch.cuda.current_stream()
-            elif _stream(stream) != self.ws_stream.cuda_stream:
-                now = torch.cuda.current_stream()
+            return self._ordered(prob, stream)
+
+    def _ordered(self, prob, stream):
+        if torch.cuda.is_current_stream_capturing():
+            return None
+        n = workspace_size(prob)
+        if self.ws is not None and _stream(stream) != self.ws_handle:
+            now = torch.cuda.current_stream()
+            with torch.cuda.stream(self.ws_stream):
+                captured = torch.cuda.is_current_stream_capturing()
+            if captured:  # (to wait for it would make this call a part of the graph)
+                self.ws = None
+            else:
                 now.wait_stream(self.ws_stream)
                 self.ws.record_stream(now)
-                self.ws_stream = now
+                self.ws_stream, self.ws_handle = now, now.cuda_stream
+        if self.ws is None or self.ws.numel() < n:
+            self.ws = None  # (freed first: the new one may take its place)
+            self.ws, self.ws_stream = torch.empty(n, dtype=torch.uint8, device=self.device), torch.cuda.current_stream()
+            self.ws_handle = self.ws_stream.cuda_stream
         return self.ws
 
     def __call__(self, x, y=None, topk_ids=None, topk_w=None, stream=None):
         prob = self.problem(x.shape[0])
         _need_tokens(prob, x, y, topk_ids, topk_w)
-        ws = self._reserve(x.shape[0], stream)
+        ws = self._reserve(prob, stream)
         w_router, bias, wg, wu, wd, s_wg, s_wu, s_wd, scales = self.w
         norm_weight, norm_eps, shared_gate = self.opts
         block = norm_weight is not None or shared_gate is not None

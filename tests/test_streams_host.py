@@ -118,7 +118,7 @@ def test_a_layers_workspace_is_ordered_between_streams_and_never_a_graphs(record
     captured call allocates for itself, so that a later growth takes nothing
     from its graph."""
     allocs, launches = recorded
-    waits, state = [], {"capturing": False}
+    waits, state = [], {"capturing": None}
 
     class S(Stream):
         def wait_stream(self, other):
@@ -140,7 +140,7 @@ def test_a_layers_workspace_is_ordered_between_streams_and_never_a_graphs(record
     monkeypatch.setattr(torch.cuda, "stream", use)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: stack[-1])
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: state["capturing"])
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: stack[-1] is state["capturing"])
     monkeypatch.setattr(moe, "_stream", lambda stream=None: (stream or stack[-1]).cuda_stream)
     monkeypatch.setattr(moe, "_device", lambda *a, **kw: torch.device("cuda", 0))
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: None)
@@ -148,7 +148,7 @@ def test_a_layers_workspace_is_ordered_between_streams_and_never_a_graphs(record
     monkeypatch.setattr(torch, "empty", lambda *a, device=None, **kw: empty(*a, **kw))
     layer = _layer()
     layer.device = torch.device("cuda", 0)
-    layer._reserve(T)
+    layer._reserve(layer.problem(T))
     ws = layer.ws
     x, y = torch.zeros((T, D), dtype=torch.bfloat16), torch.zeros((T, D), dtype=torch.bfloat16)
     used = []
@@ -160,11 +160,14 @@ def test_a_layers_workspace_is_ordered_between_streams_and_never_a_graphs(record
     assert [u[0] is ws for u in used] == [True] * 4 and [u[1] for u in used] == [None, s1, s1, s2]
     assert waits == [(41, 40), (42, 41)]
     used.clear()
-    state["capturing"] = True
+    state["capturing"] = s1
     allocs.clear()
     layer(x, y, stream=s1)
     assert used[0][0] is not ws and allocs == [s1] and layer.ws is ws and waits[2:] == []
-    state["capturing"] = False
+    state["capturing"] = None
     x = torch.zeros((4 * T, D), dtype=torch.bfloat16)
     layer(x, torch.zeros_like(x), stream=s1)  # grows on the stream that uses it
-    assert layer.ws is not ws and allocs[1:] == [s1] and layer.ws_stream is s1 and waits[2:] == []
+    assert layer.ws is not ws and allocs[1:] == [s1] and layer.ws_stream is s1 and waits[2:] == [(41, 42)]
+    state["capturing"], ws = s1, layer.ws
+    layer(x, torch.zeros_like(x), stream=s2)  # a wait for s1 would join its capture
+    assert layer.ws is not ws and allocs[2:] == [s2] and layer.ws_stream is s2 and waits[3:] == []
