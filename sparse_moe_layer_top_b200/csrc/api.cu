@@ -1981,6 +1981,7 @@ extern "C" moe_status moe_decode_forward(const moe_problem* p, const moe_block_o
   a.x = (const bf16*)x;
   a.gamma = (const bf16*)norm_w;
   a.eps = norm_w ? opt->norm_eps : 0.f;
+  a.inv_d = 1.0 / p->d;
   a.w_router = (const bf16*)w_router;
   a.bias = router_bias;
   a.wg = (const uint8_t*)w.wg;

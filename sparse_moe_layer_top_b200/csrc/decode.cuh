@@ -69,6 +69,7 @@ struct DecodeArgs {
   const bf16* x;        // [T, d] the block's input
   const bf16* gamma;    // [d] RMSNorm weight, or NULL
   float eps;
+  double inv_d;         // 1 / d
   const bf16* gate_w;   // [d] shared expert's gate, or NULL
   const bf16* w_router; // [E, d]
   const float* bias;    // [E] or NULL
@@ -524,9 +525,10 @@ __global__ void __launch_bounds__(kDecodeThreads, 1) k_decode_route(const Decode
     if (tid < a.T) {
       double v = 0.0;
       for (int w = 0; w < wpt; ++w) v += s_sq[tid * wpt + w];
-      const double r = 1.0 / sqrt(v / a.d + a.eps);
-      const float hi = (float)r;
-      s_r[tid] = make_float2(hi, isfinite(hi) ? (float)(r - hi) : 0.f);
+      const double m = v * a.inv_d + a.eps;
+      const float r = 1.0f / sqrtf((float)m);
+      // (one Newton step from r, whose second term is what r lacks)
+      s_r[tid] = make_float2(r, r > 0.f && isfinite(r) ? (float)(0.5 * r * (1.0 - m * r * r)) : 0.f);
     }
     __syncthreads();
   }

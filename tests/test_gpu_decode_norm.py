@@ -37,3 +37,32 @@ def test_the_normalised_input_is_the_64_bit_one_rounded(T, d, std):
         want = torch.softmax(xn[:, c:c + E], 1)
         worst = max(worst, ((got - want).abs() / want).max().item())
     assert worst <= 2.0 ** -20
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_rows_of_zeros_infinities_and_extremes_are_the_stage_calls(eps):
+    """Where the sum of squares is 0, infinite or NaN the normalised row is
+    moe.rmsnorm's: zeros, NaN, or zeros beside the NaN of the infinity itself."""
+    d, E, k = 264, 6, 2
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(7, d, generator=g)
+    x[0] = 0
+    x[1, 9] = float("inf")
+    x[2, 9] = float("nan")
+    x[3] *= 1e30  # squares past fp32
+    x[4] *= 1e-30  # and below it
+    x[5, 1:] = 0
+    r = lambda *s: (torch.randn(*s, generator=g) * 0.1).to(torch.bfloat16).cuda()
+    x, wr, gamma = x.to(torch.bfloat16).cuda(), r(E, d), r(d)
+    W = r(E, 16, d), r(E, 16, d), r(E, d, 16)
+    prob = moe.Problem.make(7, d, E, k, 16, 0, "bf16", "bf16")
+    out = []
+    for xi, kw in ((x, dict(norm_weight=gamma, norm_eps=eps)), (moe.rmsnorm(prob, x, gamma, eps), {})):
+        ids = torch.empty((7, k), dtype=torch.int32, device="cuda")
+        out.append((moe.decode_forward(prob, xi, wr, None, *W, topk_ids=ids, **kw), ids))
+    assert torch.equal(out[0][1], out[1][1])
+    # (finite rows: a step of bf16 of x and of y apart at most, 2^-6 of the row's largest)
+    a, b = out[0][0].float(), out[1][0].float()
+    assert torch.equal(a.isnan(), b.isnan()) and torch.equal(a.isinf(), b.isinf())
+    a, b = a.nan_to_num(0, 0, 0), b.nan_to_num(0, 0, 0)
+    assert ((a - b).abs() <= 2.0 ** -6 * b.abs().amax(1, keepdim=True)).all()
