@@ -752,7 +752,9 @@ class MoELayer:
                         shared_gate, y, topk_ids, topk_w, ws, stream, block)
 
     def decode(self, x, y=None, topk_ids=None, topk_w=None, stream=None):
-        """The block on x [T, d], T <= DECODE_MAX_T, in the latency form (decode_forward).
+        """The block on x [T, d], T <= DECODE_MAX_T, in the latency form (decode_forward):
+        the faster one for bf16 and E4M3 weights; with 4-bit weights up to 8 tokens, from
+        about 10 on calling the layer is as fast or faster.
         The workspace is each call's own, from the pool of its stream or,
         under capture, of its graph: calls on several streams may run at once."""
         prob = self.problem(x.shape[0])

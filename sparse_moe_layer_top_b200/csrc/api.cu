@@ -1858,7 +1858,7 @@ moe_status moe_ep_expand_ids(const int32_t* counts, int32_t G, int32_t E_local, 
 
 }  // extern "C"
 
-// ============================================================== a few tokens, one kernel
+// ============================================================== a few tokens, two kernels
 // Workspace of moe_decode_forward.
 struct DecodeLayout {
   size_t bar = 0, logits = 0, xn = 0, gate = 0, h = 0, xq = 0, xsc = 0, hq = 0, hsc = 0, total = 0;
