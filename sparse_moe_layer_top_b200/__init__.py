@@ -25,6 +25,7 @@ several GPUs (expert parallelism).
 import contextlib
 import ctypes
 import os
+import threading
 import warnings
 
 import torch
@@ -701,12 +702,19 @@ class MoELayer:
         self.device = wg.device
         # the workspace, and the stream of the last call that used it
         self.ws = self.ws_stream = self.ws_handle = None
+        self.lock = threading.Lock()
         if max_tokens:
             self._reserve(self.problem(max_tokens))
 
     def problem(self, T):
         d, E, k, I, I_s, act, w = self.shape
         return Problem.make(T, d, E, k, I, I_s, act, w)
+
+    def __getstate__(self):  # a copy has its own workspace
+        return {**self.__dict__, "ws": None, "ws_stream": None, "ws_handle": None, "lock": None}
+
+    def __setstate__(self, state):
+        self.__dict__.update(state, lock=threading.Lock())
 
     def _reserve(self, prob, stream=None):
         """The workspace of a call on `stream`.  One buffer serves the calls of every
@@ -744,12 +752,13 @@ class MoELayer:
     def __call__(self, x, y=None, topk_ids=None, topk_w=None, stream=None):
         prob = self.problem(x.shape[0])
         _need_tokens(prob, x, y, topk_ids, topk_w)
-        ws = self._reserve(prob, stream)
         w_router, bias, wg, wu, wd, s_wg, s_wu, s_wd, scales = self.w
         norm_weight, norm_eps, shared_gate = self.opts
         block = norm_weight is not None or shared_gate is not None
-        return _forward(prob, x, w_router, bias, wg, wu, wd, s_wg, s_wu, s_wd, scales, norm_weight, norm_eps,
-                        shared_gate, y, topk_ids, topk_w, ws, stream, block)
+        with self.lock:  # (another thread's call waits for launches, so these are queued first)
+            ws = self._reserve(prob, stream)
+            return _forward(prob, x, w_router, bias, wg, wu, wd, s_wg, s_wu, s_wd, scales, norm_weight, norm_eps,
+                            shared_gate, y, topk_ids, topk_w, ws, stream, block)
 
     def decode(self, x, y=None, topk_ids=None, topk_w=None, stream=None):
         """The block on x [T, d], T <= DECODE_MAX_T, in the latency form (decode_forward):

@@ -106,3 +106,31 @@ def test_a_layers_forward_on_side_streams_and_in_a_graph(w):
     assert torch.equal(big, want) and torch.equal(y, want_small)
     assert all(torch.equal(o, want) for o in outs)
     assert moe.device_status()[0] == 0
+
+
+@pytest.mark.parametrize("method", ["forward", "decode"])
+def test_one_layer_from_two_threads(method):
+    import threading
+    inp, W, scales = _inputs("mx4")
+    layer = moe.MoELayer(D, E, K, I, I_S, inp.w_r, *W, scales=scales, w="mx4", max_tokens=T)
+    xs = [inp.x, inp.x[:70].clone()] if method == "forward" else [inp.x[:3].clone(), inp.x[5:16].clone()]
+    call = layer if method == "forward" else layer.decode
+    want = [call(x) for x in xs]
+    torch.cuda.synchronize()
+    bad, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+
+    def work(i):
+        try:
+            with torch.cuda.stream(streams[i]):
+                for _ in range(40):
+                    if not torch.equal(call(xs[i]), want[i]):
+                        bad.append(i)
+        except Exception as e:
+            bad.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad and moe.device_status()[0] == 0

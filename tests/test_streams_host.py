@@ -171,3 +171,17 @@ def test_a_layers_workspace_is_ordered_between_streams_and_never_a_graphs(record
     state["capturing"], ws = s1, layer.ws
     layer(x, torch.zeros_like(x), stream=s2)  # a wait for s1 would join its capture
     assert layer.ws is not ws and allocs[2:] == [s2] and layer.ws_stream is s2 and waits[3:] == []
+
+
+def test_a_layer_queues_one_call_at_a_time_and_can_be_copied(recorded, monkeypatch):
+    import copy
+    import pickle
+    layer = _layer()
+    x, y = torch.zeros((T, D), dtype=torch.bfloat16), torch.zeros((T, D), dtype=torch.bfloat16)
+    held = []
+    monkeypatch.setattr(moe, "_forward_call", lambda *a: held.append(layer.lock.locked()))
+    layer(x, y)
+    assert held == [True] and not layer.lock.locked()
+    for other in (copy.copy(layer), copy.deepcopy(layer), pickle.loads(pickle.dumps(layer))):
+        assert other.ws is None and other.lock is not layer.lock and not other.lock.locked()
+        assert torch.equal(other.w[2], layer.w[2]) and other.shape == layer.shape
